@@ -1,10 +1,12 @@
 // C ABI of the qlin library: argument validation, status codes, dispatch.
 // Nothing here computes the layer; it checks arguments and enqueues kernels.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <vector>
 
 #include "qlin_internal.cuh"
+#include "qlin_kv.cuh"
 
 namespace qlin {
 
@@ -20,6 +22,8 @@ qlin_status record_cuda(cudaError_t e) {
 }
 
 static bool width_ok(int b) { return b == 3 || b == 4 || b == 6 || b == 8; }
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -81,8 +85,8 @@ const char* qlin_status_string(qlin_status s) {
   switch (s) {
     case QLIN_OK: return "QLIN_OK";
     case QLIN_ERR_INVALID_ARG: return "QLIN_ERR_INVALID_ARG: null pointer or inconsistent descriptor";
-    case QLIN_ERR_UNSUPPORTED: return "QLIN_ERR_UNSUPPORTED: code width must be 3, 4, 6 or 8";
-    case QLIN_ERR_SHAPE: return "QLIN_ERR_SHAPE: K must be a positive multiple of 128, N >= 1 (mixed: N % 64 == 0), M in range";
+    case QLIN_ERR_UNSUPPORTED: return "QLIN_ERR_UNSUPPORTED: code width must be 3, 4, 6 or 8 (cache: 4 or 8 each side, or 16 both)";
+    case QLIN_ERR_SHAPE: return "QLIN_ERR_SHAPE: K must be a positive multiple of 128, N >= 1 (mixed: N % 64 == 0), M in range (cache and norm: see their sizes in qlin.h)";
     case QLIN_ERR_ALIGNMENT: return "QLIN_ERR_ALIGNMENT: buffers must be 16-byte aligned";
     case QLIN_ERR_CUDA: return "QLIN_ERR_CUDA: a CUDA call failed (see qlin_last_cuda_error)";
     case QLIN_ERR_WORKSPACE: return "QLIN_ERR_WORKSPACE: workspace missing or too small";
@@ -242,8 +246,9 @@ size_t qlin_gemm_workspace_bytes(const qlin_desc* d, int32_t M) {
 qlin_status qlin_device_error(uint32_t* code) {
   if (!code) return QLIN_ERR_INVALID_ARG;
   const unsigned a = take_gemv_error(), b = take_gemm_error(), c = take_imma_error(), d = take_tc_error();
-  if (a == ~0u || b == ~0u || c == ~0u || d == ~0u) return QLIN_ERR_CUDA;
-  *code = a | c | (b << 8) | (d << 16);
+  const unsigned e = take_kv_error(), f = take_attn_error();
+  if (a == ~0u || b == ~0u || c == ~0u || d == ~0u || e == ~0u || f == ~0u) return QLIN_ERR_CUDA;
+  *code = a | c | (b << 8) | (d << 16) | ((e | f) << 24);
   return QLIN_OK;
 }
 
@@ -287,6 +292,101 @@ qlin_status qlin_linear_host(const qlin_desc* d, const void* packed, const uint1
                          sign_bits, xs, ys, M, workspace, s);
   if (r != QLIN_OK) return r;
   return record_cuda(cudaMemcpyAsync(y_host, y_dev, (size_t)M * (size_t)d->N * 2, cudaMemcpyDeviceToHost, s));
+}
+
+static qlin_status check_kv(const qlin_kv_desc* d) {
+  if (!d) return QLIN_ERR_INVALID_ARG;
+  if (d->num_pages < 1 || d->page_size < kPageUnit || d->page_size % kPageUnit || d->kv_heads < 1)
+    return QLIN_ERR_SHAPE;
+  if (d->head_dim != kGroup && d->head_dim != 2 * kGroup) return QLIN_ERR_SHAPE;
+  if ((int64_t)d->num_pages * d->page_size > 0x7fffffffLL) return QLIN_ERR_SHAPE;  // a slot is an int32
+  const int k = d->k_bits, v = d->v_bits;
+  const bool coded = (k == 4 || k == 8) && (v == 4 || v == 8);
+  return coded || (k == 16 && v == 16) ? QLIN_OK : QLIN_ERR_UNSUPPORTED;
+}
+
+size_t qlin_kv_cache_bytes(const qlin_kv_desc* d) {
+  if (check_kv(d) != QLIN_OK) return 0;
+  return (size_t)make_kv_view(d, nullptr).block_bytes * (size_t)d->num_pages * (size_t)d->kv_heads;
+}
+
+// Token rows of k, v or q: at least the heads' width apart, 16-byte aligned.
+static bool row_stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
+
+qlin_status qlin_kv_write(const qlin_kv_desc* d, void* cache, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                          int64_t v_stride, const int32_t* slots, int32_t T, const uint32_t* sign_bits,
+                          qlin_stream_t st) {
+  qlin_status r = check_kv(d);
+  if (r != QLIN_OK) return r;
+  if (!cache || !k || !v || !slots) return QLIN_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)d->kv_heads * d->head_dim;
+  if (T < 1 || !row_stride_ok(k_stride, width) || !row_stride_ok(v_stride, width)) return QLIN_ERR_SHAPE;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v) || !aligned4(slots) || !aligned16(sign_bits))
+    return QLIN_ERR_ALIGNMENT;
+  return launch_kv_write(make_kv_view(d, cache), reinterpret_cast<const __half*>(k),
+                         reinterpret_cast<const __half*>(v), k_stride, v_stride, slots, T, sign_bits,
+                         reinterpret_cast<cudaStream_t>(st));
+}
+
+qlin_status qlin_kv_read(const qlin_kv_desc* d, const void* cache, const int32_t* slots, int32_t T,
+                         const uint32_t* sign_bits, uint16_t* k, uint16_t* v, qlin_stream_t st) {
+  qlin_status r = check_kv(d);
+  if (r != QLIN_OK) return r;
+  if (!cache || !k || !v || !slots || k == v) return QLIN_ERR_INVALID_ARG;
+  if (T < 1) return QLIN_ERR_SHAPE;
+  if (!aligned16(cache) || !aligned16(k) || !aligned16(v) || !aligned4(slots) || !aligned16(sign_bits))
+    return QLIN_ERR_ALIGNMENT;
+  return launch_kv_read(make_kv_view(d, cache), reinterpret_cast<__half*>(k), reinterpret_cast<__half*>(v), slots, T,
+                        sign_bits, reinterpret_cast<cudaStream_t>(st));
+}
+
+// Sizes of an attention call; the tiles of 16 tokens over all heads and
+// sequences are counted in an int32.
+static qlin_status check_attn(const qlin_kv_desc* d, int32_t q_heads, int32_t B, int32_t max_pages) {
+  qlin_status r = check_kv(d);
+  if (r != QLIN_OK) return r;
+  if (B < 1 || max_pages < 1 || q_heads < 1 || q_heads % d->kv_heads) return QLIN_ERR_SHAPE;
+  const int64_t tokens = (int64_t)max_pages * d->page_size;
+  if (tokens > 0x7fffffffLL || (int64_t)B * q_heads > 0x7fffffffLL) return QLIN_ERR_SHAPE;
+  if ((double)(tokens / kPageUnit) * (double)B * (double)q_heads > 2147483647.0) return QLIN_ERR_SHAPE;
+  return QLIN_OK;
+}
+
+size_t qlin_attn_workspace_bytes(const qlin_kv_desc* d, int32_t q_heads, int32_t B, int32_t max_pages) {
+  return check_attn(d, q_heads, B, max_pages) == QLIN_OK ? attn_workspace_bytes(d, q_heads, B, max_pages) : 0;
+}
+
+qlin_status qlin_attn_decode(const qlin_kv_desc* d, const void* cache, const uint16_t* q, int64_t q_stride,
+                             int32_t q_heads, const int32_t* block_table, int32_t max_pages, const int32_t* seq_lens,
+                             int32_t B, const uint32_t* sign_bits, float scale, uint16_t* out, void* workspace,
+                             size_t workspace_bytes, qlin_stream_t st) {
+  qlin_status r = check_attn(d, q_heads, B, max_pages);
+  if (r != QLIN_OK) return r;
+  if (!cache || !q || !block_table || !seq_lens || !out || q == out || !std::isfinite(scale))
+    return QLIN_ERR_INVALID_ARG;
+  if (!row_stride_ok(q_stride, (int64_t)q_heads * d->head_dim)) return QLIN_ERR_SHAPE;
+  if (!aligned16(cache) || !aligned16(q) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned16(out) ||
+      !aligned16(sign_bits))
+    return QLIN_ERR_ALIGNMENT;
+  const size_t ws = attn_workspace_bytes(d, q_heads, B, max_pages);
+  if (ws && (!workspace || workspace_bytes < ws)) return QLIN_ERR_WORKSPACE;
+  if (ws && !aligned16(workspace)) return QLIN_ERR_ALIGNMENT;
+  return launch_attn_decode(make_kv_view(d, cache), reinterpret_cast<const __half*>(q), q_stride, q_heads,
+                            block_table, max_pages, seq_lens, B, sign_bits, scale, reinterpret_cast<__half*>(out),
+                            workspace, reinterpret_cast<cudaStream_t>(st));
+}
+
+qlin_status qlin_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, uint16_t* y,
+                         uint16_t* residual_out, int32_t M, int32_t K, qlin_stream_t st) {
+  if (!x || !weight || !y || (residual == nullptr) != (residual_out == nullptr)) return QLIN_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return QLIN_ERR_INVALID_ARG;
+  if (M < 1 || K < 8 || K % 8 || K > 65536) return QLIN_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(y) || !aligned16(residual_out))
+    return QLIN_ERR_ALIGNMENT;
+  if (y == x || (residual && (y == residual || y == residual_out || residual_out == x))) return QLIN_ERR_INVALID_ARG;
+  return launch_rmsnorm(reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(residual),
+                        reinterpret_cast<const __half*>(weight), eps, reinterpret_cast<__half*>(y),
+                        reinterpret_cast<__half*>(residual_out), M, K, reinterpret_cast<cudaStream_t>(st));
 }
 
 }  // extern "C"

@@ -85,6 +85,20 @@ qlin_status launch_gemm(const PackedView& v, const __half* scales, const __half*
                         const uint32_t* sign_bits, const __half* x, __half* y, int M,
                         void* workspace, cudaStream_t s);
 
+// The decode step between the linear layers: the paged key/value cache
+// (qlin_kv.cuh), attention of one new token over it, and the norm.
+struct KvView;
+qlin_status launch_kv_write(const KvView& c, const __half* k, const __half* v, int64_t k_stride, int64_t v_stride,
+                            const int32_t* slots, int tokens, const uint32_t* sign_bits, cudaStream_t s);
+qlin_status launch_kv_read(const KvView& c, __half* k, __half* v, const int32_t* slots, int tokens,
+                           const uint32_t* sign_bits, cudaStream_t s);
+size_t attn_workspace_bytes(const qlin_kv_desc* d, int q_heads, int batch, int max_pages);
+qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_stride, int q_heads,
+                               const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
+                               const uint32_t* sign_bits, float scale, __half* out, void* workspace, cudaStream_t s);
+qlin_status launch_rmsnorm(const __half* x, const __half* residual, const __half* weight, float eps, __half* y,
+                           __half* residual_out, int M, int K, cudaStream_t s);
+
 // ---------------------------------------------------------------------------
 // Device decode routines
 // ---------------------------------------------------------------------------

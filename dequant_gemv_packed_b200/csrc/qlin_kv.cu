@@ -1,0 +1,276 @@
+// qlin_kv_write and qlin_kv_read: quantising keys and values into the paged
+// cache as they are written, and reading them back.
+//
+// Per group of 128 values (one Hadamard block, one scale and zero): the vector
+// is rotated like an activation ("24B0978-Week01-Track2_20-Submission01",
+// paragraph "Random Hadamard transform"), then quantised by the affine form of
+// "Group-wise affine integer quantisation" on a grid that contains zero,
+//   lo = min(v, 0), hi = max(v, 0), s = fp16 up((hi - lo) / qmax),
+//   z = fp16(-lo / s), q = clamp(rint(v / s + z), 0, qmax),  value = s (q - z).
+// Zero on the grid keeps z inside [0, qmax] for every input, so fp16 holds it to
+// 1/16 of a step or better (a group far from zero would otherwise overflow z);
+// rounding s up keeps hi on the grid where s is subnormal (values of 1e-4 and
+// below, where rounding to nearest could drop several per cent of the range).
+// Every step is one IEEE fp32 operation and the butterfly strides run 1, 2, ...,
+// 64, so the stored bytes are a function of the input alone.
+//
+// Eight lanes a group, 16 consecutive values each: strides 1 to 8 in the lane,
+// 16 to 64 over lane distances 1, 2, 4.
+#include "qlin_kv.cuh"
+
+namespace qlin {
+namespace {
+
+__device__ unsigned int g_kv_error;
+
+constexpr int kThreads = 256;
+constexpr int kTasksPerCta = kThreads / 8;
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Butterflies of strides 1..64 over the 16 values of each of a group's eight lanes.
+__device__ __forceinline__ void fwht128_oct(float (&v)[16], int t) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (!(j & h)) {
+        const float a = v[j], b = v[j + h];
+        v[j] = __fadd_rn(a, b);
+        v[j + h] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const bool upper = (t & o) != 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float p = __shfl_xor_sync(0xffffffffu, v[j], o);
+      v[j] = upper ? __fsub_rn(p, v[j]) : __fadd_rn(v[j], p);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], kInvSqrt128);
+}
+
+__device__ __forceinline__ void flip16(float (&v)[16], uint32_t sw) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    v[j] = __uint_as_float(__float_as_uint(v[j]) ^ (((sw >> j) & 1u) << 31));
+}
+
+__device__ __forceinline__ void halves_to_float(const uint4& r0, const uint4& r1, float (&v)[16]) {
+  const uint32_t raw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ void float_to_halves(const float (&v)[16], uint4& r0, uint4& r1) {
+  uint32_t raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    raw[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  r0 = make_uint4(raw[0], raw[1], raw[2], raw[3]);
+  r1 = make_uint4(raw[4], raw[5], raw[6], raw[7]);
+}
+
+struct KvArgs {
+  KvView c;
+  const __half *k_in, *v_in;  // write: token rows
+  __half *k_out, *v_out;      // read: token rows
+  int64_t k_stride, v_stride; // elements between tokens
+  const int32_t* slots;
+  const uint32_t* sign_bits;  // null: not rotated
+  int32_t tokens;
+};
+
+// A task is one group of one token, head and side: order (token, head, side, group).
+struct Task {
+  bool live;
+  int side, g, bits, slot;
+  int64_t in;     // element offset of the group in the token rows (without the lane's 16 t)
+  uint8_t* row;   // the group's codes in the cache
+  uint8_t* par;   // the group's (scale, zero) pair of this side
+};
+
+__device__ __forceinline__ Task find_task(const KvArgs& a, int t, int64_t stride_k, int64_t stride_v) {
+  Task k;
+  const int groups = a.c.dim / kGroup;
+  const int64_t total = (int64_t)a.tokens * a.c.heads * 2 * groups;
+  const int64_t id = (int64_t)blockIdx.x * kTasksPerCta + (threadIdx.x >> 3);
+  k.live = id < total;
+  int64_t i = k.live ? id : total - 1;
+  k.g = (int)(i % groups);
+  i /= groups;
+  k.side = (int)(i & 1);
+  i >>= 1;
+  const int h = (int)(i % a.c.heads);
+  const int tok = (int)(i / a.c.heads);
+  k.bits = k.side ? a.c.v_bits : a.c.k_bits;
+  k.in = (int64_t)tok * (k.side ? stride_v : stride_k) + (int64_t)h * a.c.dim + (int64_t)k.g * kGroup;
+  k.slot = a.slots[tok];
+  if (k.slot >= a.c.pages * a.c.page) {
+    if (t == 0) atomicOr(&g_kv_error, kKvBadSlot);
+    k.slot = -1;
+  }
+  const int s = k.slot < 0 ? 0 : k.slot;
+  uint8_t* b = a.c.pool + ((int64_t)(s / a.c.page) * a.c.heads + h) * a.c.block_bytes;
+  const int off = s % a.c.page;
+  k.row = b + (k.side ? a.c.v_offset() + (int64_t)off * a.c.v_row : (int64_t)off * a.c.k_row) +
+          (int64_t)k.g * (kGroup / 8) * k.bits;
+  k.par = b + a.c.par_offset() + (int64_t)off * a.c.par + 8 * k.g + 4 * k.side;
+  return k;
+}
+
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
+  const int t = threadIdx.x & 7;
+  const Task k = find_task(a, t, a.k_stride, a.v_stride);
+  const __half* src = (k.side ? a.v_in : a.k_in) + k.in + 16 * t;
+  uint4 r0 = reinterpret_cast<const uint4*>(src)[0];
+  uint4 r1 = reinterpret_cast<const uint4*>(src)[1];
+  float v[16];
+  halves_to_float(r0, r1, v);
+  if (a.sign_bits) {
+    flip16(v, a.sign_bits[k.g * 4 + (t >> 1)] >> (16 * (t & 1)));
+    fwht128_oct(v, t);
+  }
+  const bool store = k.live && k.slot >= 0;
+  if (k.bits == 16) {  // both sides, or neither: uniform over the grid
+    if (a.sign_bits) float_to_halves(v, r0, r1);
+    if (store) {
+      reinterpret_cast<uint4*>(k.row)[2 * t] = r0;
+      reinterpret_cast<uint4*>(k.row)[2 * t + 1] = r1;
+    }
+    return;
+  }
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    lo = min_nan(lo, v[j]);
+    hi = max_nan(hi, v[j]);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  lo = __fadd_rn(lo, 0.f);  // a zero bound is +0 whichever zero the reduction kept
+  const float qmax = (float)((1 << k.bits) - 1);
+  const float span = __fdiv_rn(__fsub_rn(hi, lo), qmax);
+  const bool finite = span < INFINITY;  // false for NaN too
+  __half s16 = __float2half_ru(fminf(span, 65504.f));
+  if (!(span > 0.f) || !finite) s16 = __float2half_rn(1.f);
+  const float s = __half2float(s16);
+  // a group that holds an infinity or NaN reads back as NaN throughout
+  const __half z16 = finite ? __float2half_rn(__fdiv_rn(-lo, s)) : __ushort_as_half(0x7fff);
+  const float z = __half2float(z16);
+  uint32_t q[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    q[j] = (uint32_t)fminf(fmaxf(rintf(__fadd_rn(__fdiv_rn(v[j], s), z)), 0.f), qmax);
+  if (!store) return;
+  if (k.bits == 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = q[4 * i] | q[4 * i + 1] << 8 | q[4 * i + 2] << 16 | q[4 * i + 3] << 24;
+    reinterpret_cast<uint4*>(k.row)[t] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j >> 3] |= q[j] << (4 * (j & 7));
+    reinterpret_cast<uint2*>(k.row)[t] = make_uint2(w[0], w[1]);
+  }
+  if (t == 0) *reinterpret_cast<__half2*>(k.par) = __halves2half2(s16, z16);
+}
+
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
+  const int t = threadIdx.x & 7;
+  const int64_t row = (int64_t)a.c.heads * a.c.dim;
+  const Task k = find_task(a, t, row, row);
+  uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+  float v[16];
+  if (k.bits == 16) {
+    r0 = reinterpret_cast<const uint4*>(k.row)[2 * t];
+    r1 = reinterpret_cast<const uint4*>(k.row)[2 * t + 1];
+    halves_to_float(r0, r1, v);
+  } else {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(k.par));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (k.bits == 8) {
+      const uint4 c = reinterpret_cast<const uint4*>(k.row)[t];
+      w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        v[j] = __fmul_rn(p.x, __fsub_rn((float)((w[j >> 2] >> (8 * (j & 3))) & 255u), p.y));
+    } else {
+      const uint2 c = reinterpret_cast<const uint2*>(k.row)[t];
+      w[0] = c.x, w[1] = c.y;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        v[j] = __fmul_rn(p.x, __fsub_rn((float)((w[j >> 3] >> (4 * (j & 7))) & 15u), p.y));
+    }
+  }
+  if (a.sign_bits) {
+    fwht128_oct(v, t);
+    flip16(v, a.sign_bits[k.g * 4 + (t >> 1)] >> (16 * (t & 1)));
+  }
+  if (a.sign_bits || k.bits != 16) float_to_halves(v, r0, r1);
+  if (k.slot < 0) r0 = r1 = make_uint4(0u, 0u, 0u, 0u);
+  if (!k.live) return;
+  uint4* dst = reinterpret_cast<uint4*>((k.side ? a.v_out : a.k_out) + k.in + 16 * t);
+  dst[0] = r0;
+  dst[1] = r1;
+}
+
+}  // namespace
+
+unsigned take_kv_error() {
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_kv_error, sizeof(v)) != cudaSuccess) return ~0u;
+  if (v) cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(zero));
+  return v;
+}
+
+static qlin_status kv_grid(const KvArgs& a, unsigned* grid) {
+  const int64_t tasks = (int64_t)a.tokens * a.c.heads * 2 * (a.c.dim / kGroup);
+  const int64_t g = (tasks + kTasksPerCta - 1) / kTasksPerCta;
+  if (g > 0x7fffffffLL) return QLIN_ERR_SHAPE;
+  *grid = (unsigned)g;
+  return QLIN_OK;
+}
+
+qlin_status launch_kv_write(const KvView& c, const __half* k, const __half* v, int64_t k_stride, int64_t v_stride,
+                            const int32_t* slots, int tokens, const uint32_t* sign_bits, cudaStream_t s) {
+  const KvArgs a = {c, k, v, nullptr, nullptr, k_stride, v_stride, slots, sign_bits, tokens};
+  unsigned grid;
+  const qlin_status r = kv_grid(a, &grid);
+  if (r != QLIN_OK) return r;
+  kv_write_kernel<<<grid, kThreads, 0, s>>>(a);
+  return record_cuda(cudaGetLastError());
+}
+
+qlin_status launch_kv_read(const KvView& c, __half* k, __half* v, const int32_t* slots, int tokens,
+                           const uint32_t* sign_bits, cudaStream_t s) {
+  const KvArgs a = {c, nullptr, nullptr, k, v, 0, 0, slots, sign_bits, tokens};
+  unsigned grid;
+  const qlin_status r = kv_grid(a, &grid);
+  if (r != QLIN_OK) return r;
+  kv_read_kernel<<<grid, kThreads, 0, s>>>(a);
+  return record_cuda(cudaGetLastError());
+}
+
+}  // namespace qlin

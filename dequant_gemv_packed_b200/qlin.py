@@ -24,6 +24,8 @@ EXPORTED = (
     "qlin_unpack", "qlin_dequant", "qlin_rht", "qlin_gemv_workspace_bytes", "qlin_gemv",
     "qlin_gemm_workspace_bytes", "qlin_gemm", "qlin_device_error", "qlin_gemm_noalloc", "qlin_set_overlap",
     "qlin_quantize_rtn", "qlin_gemv_plan", "qlin_gptq_workspace_bytes", "qlin_quantize_gptq", "qlin_linear_host",
+    "qlin_kv_cache_bytes", "qlin_kv_write", "qlin_kv_read", "qlin_attn_workspace_bytes", "qlin_attn_decode",
+    "qlin_rmsnorm",
 )
 
 
@@ -65,6 +67,26 @@ class Desc:
         return self._byref
 
 
+class _KVDesc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("num_pages", "page_size", "kv_heads", "head_dim", "k_bits",
+                                                    "v_bits")]
+
+
+class KVDesc:
+    """qlin_kv_desc: the paged key/value cache (see qlin.h)."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, k_bits: int, v_bits: int):
+        self.num_pages, self.page_size, self.kv_heads = int(num_pages), int(page_size), int(kv_heads)
+        self.head_dim, self.k_bits, self.v_bits = int(head_dim), int(k_bits), int(v_bits)
+        self.c = _KVDesc(self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.k_bits, self.v_bits)
+        self._byref = ctypes.byref(self.c)
+        self._bytes = None  # of the pool: a pure function of the descriptor
+        self._ws = {}  # (q_heads, B, max_pages) -> workspace bytes, likewise
+
+    def ref(self):
+        return self._byref
+
+
 _lib = None
 
 
@@ -100,6 +122,15 @@ def lib() -> ctypes.CDLL:
     L.qlin_gemm_noalloc.argtypes, L.qlin_gemm_noalloc.restype = [vp, vp, vp, vp, vp, vp, vp, i32, vp], ctypes.c_int
     L.qlin_linear_host.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
     L.qlin_linear_host.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    L.qlin_kv_cache_bytes.argtypes, L.qlin_kv_cache_bytes.restype = [vp], sz
+    L.qlin_kv_write.argtypes, L.qlin_kv_write.restype = [vp, vp, vp, vp, i64, i64, vp, i32, vp, vp], ctypes.c_int
+    L.qlin_kv_read.argtypes, L.qlin_kv_read.restype = [vp, vp, vp, i32, vp, vp, vp, vp], ctypes.c_int
+    L.qlin_attn_workspace_bytes.argtypes, L.qlin_attn_workspace_bytes.restype = [vp, i32, i32, i32], sz
+    L.qlin_attn_decode.argtypes = [vp, vp, vp, i64, i32, vp, i32, vp, i32, vp, ctypes.c_float, vp, vp, sz, vp]
+    L.qlin_attn_decode.restype = ctypes.c_int
+    L.qlin_rmsnorm.argtypes = [vp, vp, vp, ctypes.c_float, vp, vp, i32, i32, vp]
+    L.qlin_rmsnorm.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -337,6 +368,153 @@ def qlin_linear_host(desc: Desc, packed, scales, zeros, sign_bits, x_host, y_hos
                                   _dev(y_dev, torch.float16, "y_dev"), M, ws_ptr, ws_len, _stream(stream, x_dev)),
            "qlin_linear_host")
     return y_host
+
+
+# ------------------------------------------------- the decode step between the layers
+
+def _on(t: torch.Tensor, stream):
+    """Context of a call on `t`'s device and `stream`: makes the device current, and
+    allocates outputs and workspaces on the stream that uses them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("the call takes CUDA tensors: its buffers must each be a CUDA tensor")
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _same_device(like: torch.Tensor, **tensors) -> None:
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _heads(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
+    """Element stride between the token rows of t [T, heads, dim], whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {list(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    return heads * dim if t.shape[0] == 1 else t.stride(0)
+
+
+def _cache(desc: KVDesc, cache: torch.Tensor) -> int:
+    if desc._bytes is None:
+        desc._bytes = qlin_kv_cache_bytes(desc)
+    p = _dev(cache, torch.uint8, "cache")
+    if cache.numel() < desc._bytes:
+        raise ValueError("cache buffer too small")
+    return p
+
+
+def _signs(desc: KVDesc, sign_bits: Optional[torch.Tensor]):
+    if sign_bits is None:
+        return None
+    p = _dev(sign_bits, torch.int32, "sign_bits")
+    if sign_bits.numel() != desc.head_dim // 32:
+        raise ValueError("sign_bits must hold head_dim bits")
+    return p
+
+
+def qlin_kv_cache_bytes(desc: KVDesc) -> int:
+    return int(lib().qlin_kv_cache_bytes(desc.ref()))
+
+
+def qlin_kv_write(desc: KVDesc, cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                  sign_bits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Quantise the keys and values [T, kv_heads, head_dim] (rows may be columns of a wider
+    matrix) into the cache at `slots` [T] int32, negative ones skipped; returns the cache."""
+    with _on(cache, stream):
+        _same_device(cache, k=k, v=v, slots=slots, sign_bits=sign_bits)
+        ks, vs = _heads(k, desc.kv_heads, desc.head_dim, "k"), _heads(v, desc.kv_heads, desc.head_dim, "v")
+        sp = _dev(slots, torch.int32, "slots")
+        if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+            raise ValueError("k, v and slots must have one row per token")
+        _check(lib().qlin_kv_write(desc.ref(), _cache(desc, cache), k.data_ptr(), v.data_ptr(), ks, vs, sp, k.shape[0],
+                                   _signs(desc, sign_bits), _stream(stream, cache)), "qlin_kv_write")
+    return cache
+
+
+def qlin_kv_read(desc: KVDesc, cache: torch.Tensor, slots: torch.Tensor, sign_bits: Optional[torch.Tensor] = None,
+                 k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
+    """Keys and values [T, kv_heads, head_dim] fp16 at `slots` [T] int32 (zeros for negative ones)."""
+    with _on(cache, stream):
+        _same_device(cache, slots=slots, sign_bits=sign_bits, k=k, v=v)
+        sp = _dev(slots, torch.int32, "slots")
+        shape = (slots.numel(), desc.kv_heads, desc.head_dim)
+        k = _alloc(shape, torch.float16, cache) if k is None else k
+        v = _alloc(shape, torch.float16, cache) if v is None else v
+        if tuple(k.shape) != shape or tuple(v.shape) != shape:
+            raise ValueError(f"k and v must be {list(shape)}")
+        _check(lib().qlin_kv_read(desc.ref(), _cache(desc, cache), sp, shape[0], _signs(desc, sign_bits),
+                                  _dev(k, torch.float16, "k"), _dev(v, torch.float16, "v"), _stream(stream, cache)),
+               "qlin_kv_read")
+    return k, v
+
+
+def qlin_attn_workspace_bytes(desc: KVDesc, q_heads: int, B: int, max_pages: int) -> int:
+    return int(lib().qlin_attn_workspace_bytes(desc.ref(), q_heads, B, max_pages))
+
+
+def qlin_attn_decode(desc: KVDesc, cache: torch.Tensor, q: torch.Tensor, block_table: torch.Tensor,
+                     seq_lens: torch.Tensor, scale: Optional[float] = None, sign_bits: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [B, q_heads, head_dim], over the cached tokens
+    t < seq_lens[b] (int32 [B]) in the pages block_table [B, max_pages] (int32); scale defaults
+    to 1 / sqrt(head_dim).  Returns [B, q_heads, head_dim]."""
+    with _on(cache, stream):
+        _same_device(cache, q=q, block_table=block_table, seq_lens=seq_lens, sign_bits=sign_bits, out=out,
+                     workspace=workspace)
+        if q.dim() != 3:
+            raise ValueError("q must be [B, q_heads, head_dim]")
+        B, Hq, D = q.shape
+        qs = _heads(q, Hq, desc.head_dim, "q")
+        tp, lp = _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens")
+        if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+            raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+        if out is None:
+            out = _alloc((B, Hq, D), torch.float16, q)
+        elif tuple(out.shape) != (B, Hq, D):
+            raise ValueError("out must be [B, q_heads, head_dim]")
+        mp = block_table.shape[1]
+        ws = desc._ws.get((Hq, B, mp))
+        if ws is None:
+            ws = desc._ws[(Hq, B, mp)] = qlin_attn_workspace_bytes(desc, Hq, B, mp)
+        if workspace is None and ws:
+            workspace = _alloc((ws,), torch.uint8, q)
+        wp, wl = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
+        _check(lib().qlin_attn_decode(desc.ref(), _cache(desc, cache), q.data_ptr(), qs, Hq, tp, mp, lp, B,
+                                      _signs(desc, sign_bits), desc.head_dim ** -0.5 if scale is None else scale,
+                                      _dev(out, torch.float16, "out"), wp, wl, _stream(stream, cache)),
+               "qlin_attn_decode")
+    return out
+
+
+def qlin_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                 y: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None, stream=None):
+    """Root-mean-square norm of the rows of x [M, K], after the addition of `residual` if given:
+    y, or (y, the new residual).  residual_out may be `residual` itself."""
+    with _on(x, stream):
+        _same_device(x, weight=weight, residual=residual, y=y, residual_out=residual_out)
+        M, K = x.shape
+        if weight.numel() != K or any(t is not None and tuple(t.shape) != (M, K) for t in (residual, y, residual_out)):
+            raise ValueError("shapes: x, residual, y, residual_out [M, K], weight [K]")
+        if residual is None and residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        y = torch.empty_like(x) if y is None else y
+        rp = op = None
+        if residual is not None:
+            residual_out = torch.empty_like(x) if residual_out is None else residual_out
+            rp, op = _dev(residual, torch.float16, "residual"), _dev(residual_out, torch.float16, "residual_out")
+        _check(lib().qlin_rmsnorm(_dev(x, torch.float16, "x"), rp, _dev(weight, torch.float16, "weight"), eps,
+                                  _dev(y, torch.float16, "y"), op, M, K, _stream(stream, x)), "qlin_rmsnorm")
+    return y if residual is None else (y, residual_out)
 
 
 def algorithmic_bytes(desc: Desc) -> int:

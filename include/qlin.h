@@ -364,11 +364,118 @@ qlin_status qlin_linear_host(const qlin_desc* desc, const void* packed, const ui
                              uint16_t* y_host, uint16_t* x_dev, uint16_t* y_dev, int32_t M, void* workspace,
                              size_t workspace_bytes, qlin_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The decode step between the linear layers: paged key/value cache, attention
+ * of one new token, and the norm in front of a layer
+ * ---------------------------------------------------------------------------
+ * The pages have no counterpart to these calls; they store, read and use keys
+ * and values in the pages' own terms: codes of a group of 128 with one fp16
+ * scale and zero ("24B0978-Week01-Track2_20-Submission01", paragraph "Group-wise
+ * affine integer quantisation"), after the random block-128 Hadamard transform
+ * (paragraph "Random Hadamard transform") that spreads outlying channels.
+ *
+ * Cache layout: one pool [num_pages][kv_heads][block].  A block (one page, one
+ * head) holds, for its page_size tokens in order,
+ *     K rows  [page_size][head_dim * k_bits / 8]
+ *     V rows  [page_size][head_dim * v_bits / 8]
+ *     fp16    [page_size][head_dim / 128][4] = ks, kz, vs, vz   (below 16 bits)
+ * A row of codes is qlin_pack's bit stream; at 16 bits it is the fp16 vector.
+ * A token's place is its slot, page * page_size + offset.
+ *
+ * A vector v (rotated if sign bits are given, R v = (1/sqrt(128)) H diag(d) v per
+ * block of 128, butterflies in fp32 with strides 1, 2, ..., 64, then the scaling)
+ * is stored per group of 128, every step one IEEE fp32 operation, as
+ *     lo = min(v, 0), hi = max(v, 0), qmax = 2^b - 1,
+ *     s = (hi - lo) / qmax rounded UP to fp16 (1 if that is 0, at most 65504),
+ *     z = fp16_rn(-lo / s),  q = min(max(rint(v / s + z), 0), qmax),
+ * and stands for s (q - z).  Zero lies on the grid, so z is within [0, qmax].
+ * At 16 bits the (rotated) vector is rounded to fp16.  A group that holds an
+ * infinity or NaN reads back as NaN throughout (below 16 bits). */
+typedef struct {
+  int32_t num_pages;  /* >= 1; num_pages * page_size < 2^31                    */
+  int32_t page_size;  /* tokens a page holds: a positive multiple of 16        */
+  int32_t kv_heads;   /* >= 1                                                  */
+  int32_t head_dim;   /* 128 or 256                                            */
+  int32_t k_bits;     /* 4 or 8; or 16 for both sides                          */
+  int32_t v_bits;
+} qlin_kv_desc;
+
+/* Bytes of the cache pool; 0 for an invalid descriptor. */
+size_t qlin_kv_cache_bytes(const qlin_kv_desc* desc);
+
+/* Writes T tokens' keys and values into the cache, quantising them.
+ *   k, v  : device fp16, token t's heads [kv_heads][head_dim] at element offset
+ *           t * k_stride (t * v_stride); strides >= kv_heads * head_dim and
+ *           multiples of 8, so both may be columns of one wider product;
+ *   slots : device int32 [T] (4-byte aligned): where each token goes.  A negative
+ *           slot is a padded token and is skipped; one past the pool is skipped
+ *           and sets bit 24 of qlin_device_error.  The slots of one call must
+ *           differ: two tokens at one slot leave bytes of either there;
+ *   sign_bits : device uint32 [head_dim/32], or NULL for no rotation; the cache
+ *           must be read with the same.
+ * T >= 1.  Slots that are not named keep their bytes. */
+qlin_status qlin_kv_write(const qlin_kv_desc* desc, void* cache, const uint16_t* k, const uint16_t* v,
+                          int64_t k_stride, int64_t v_stride, const int32_t* slots, int32_t T,
+                          const uint32_t* sign_bits, qlin_stream_t stream);
+
+/* Reads T tokens back: fp16_rn of s (q - z) (each fp32 operation rounded), of
+ * its inverse rotation R^T if sign_bits are given (the same butterflies, the
+ * scaling, then the signs).
+ *   k, v  : device fp16 [T][kv_heads][head_dim], written entirely; a negative
+ *           slot gives zeros, so does one past the pool, which sets bit 24 of
+ *           qlin_device_error.  A slot may occur any number of times. */
+qlin_status qlin_kv_read(const qlin_kv_desc* desc, const void* cache, const int32_t* slots, int32_t T,
+                         const uint32_t* sign_bits, uint16_t* k, uint16_t* v, qlin_stream_t stream);
+
+/* Workspace bytes of qlin_attn_decode: the partial sums of sequences whose
+ * tokens several CTAs share.  0: none is needed (or an argument is invalid). */
+size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int32_t B, int32_t max_pages);
+
+/* Attention of one new token per sequence over its cached keys and values:
+ *   out[b][h] = fp16_rn( R^T sum_t p_t v_t ),  p = softmax_t( scale * x . k_t ),
+ * over the tokens t < seq_lens[b] of sequence b, where k_t and v_t are the values
+ * s (q - z) of the cache (real numbers, never written), kv head h / (q_heads /
+ * kv_heads), x = fp16_rn(R q[b][h]) and R the rotation (R = 1 and x = q[b][h]
+ * without sign bits; the codes then are those of unrotated vectors).  Scores,
+ * softmax statistics and sums are fp32; the softmax weights enter the product
+ * with the values as fp16 (times the token's scale), in numerator and
+ * denominator alike.  Deterministic.
+ *   q     : device fp16, sequence b's heads [q_heads][head_dim] at element offset
+ *           b * q_stride; q_stride >= q_heads * head_dim, a multiple of 8;
+ *           q_heads a multiple of kv_heads;
+ *   block_table : device int32 [B][max_pages] (4-byte aligned), the page of each
+ *           page_size tokens of a sequence; entries past its length are not read.
+ *           A page outside the pool counts as absent (its tokens are masked) and
+ *           sets bit 25 of qlin_device_error;
+ *   seq_lens : device int32 [B] (4-byte aligned).  A length <= 0 gives zeros; one
+ *           beyond max_pages * page_size is cut there and sets bit 26;
+ *   out   : device fp16 [B][q_heads][head_dim], not q;
+ *   workspace : >= qlin_attn_workspace_bytes(...) bytes, overwritten; calls that
+ *           overlap on the GPU need one each.
+ * The lengths are read on the device, so a captured call follows them. */
+qlin_status qlin_attn_decode(const qlin_kv_desc* desc, const void* cache, const uint16_t* q, int64_t q_stride,
+                             int32_t q_heads, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* seq_lens, int32_t B, const uint32_t* sign_bits, float scale,
+                             uint16_t* out, void* workspace, size_t workspace_bytes, qlin_stream_t stream);
+
+/* Residual addition and root-mean-square norm, the input of a linear layer:
+ *   h = fp16_rn(x + residual)   (h = x without a residual),
+ *   y = fp16_rn( h / sqrt(mean_k h[k]^2 + eps) * weight[k] ),  in fp32.
+ *   x, y  : device fp16 [M][K];  weight : device fp16 [K];
+ *   residual, residual_out : device fp16 [M][K], the old and the new residual
+ *           stream (h); both or neither NULL; residual_out may be residual, no
+ *           other output may be an input.
+ * M >= 1, K a multiple of 8, 8 <= K <= 65536, eps >= 0 and finite. */
+qlin_status qlin_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps,
+                         uint16_t* y, uint16_t* residual_out, int32_t M, int32_t K, qlin_stream_t stream);
+
 /* Reads and clears the device-side error word (0 = no error).  Kernels that
  * wait on shared-memory barriers bound every wait; a wait that gives up sets a
  * bit here instead of hanging (the call's output is then invalid): bits 0-7
- * the M = 1 GEMV kernels, 8-15 the GEMM, 16-23 the split-K GEMV.  Synchronous:
- * waits for all work already queued on the device. */
+ * the M = 1 GEMV kernels, 8-15 the GEMM, 16-23 the split-K GEMV.  Bits 24-31:
+ * slots, pages and lengths outside the cache (qlin_kv_write, qlin_kv_read,
+ * qlin_attn_decode).  Synchronous: waits for all work already queued on the
+ * device. */
 qlin_status qlin_device_error(uint32_t* code);
 
 #ifdef __cplusplus
