@@ -269,6 +269,21 @@ def test_masked_places_may_hold_anything(kb, vb, fill):
         check_attention(run_attention(c, q, table, lens), c, q, table, lens, what=f"{lens}")
 
 
+@pytest.mark.parametrize("kb,vb", [(8, 8), (4, 4), (16, 16)])
+def test_cleared_slots_inside_a_length_are_zero_vectors(kb, vb):
+    """A slot of a zero-filled pool that was never written stands for k = v = 0: a score of 0, and a
+    share of the weights; alone in the sequence, in the first tile, and among written tokens."""
+    rng = np.random.default_rng(24)
+    c = D.Cache(6, 16, 1, 128, kb, vb)
+    n = 40
+    c.write(vectors(rng, n, 1, 128), vectors(rng, n, 1, 128), range(20, 20 + n))
+    q = (0.2 * rng.standard_normal((3, 4, 128))).astype(np.float16)
+    table, lens = np.array([[0, 1, 2, 3], [5, 5, 5, 5], [4, 1, 2, 5]]), [50, 33, 64]
+    got = run_attention(c, q, table, lens)
+    check_attention(got, c, q, table, lens)
+    assert not got[1].any()
+
+
 def test_page_outside_the_pool_is_masked_and_reported():
     rng = np.random.default_rng(15)
     c = filled(rng, 4, 16, 1, 128, 8, 8, None)
