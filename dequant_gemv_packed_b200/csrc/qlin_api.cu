@@ -341,14 +341,14 @@ qlin_status qlin_kv_read(const qlin_kv_desc* d, const void* cache, const int32_t
 }
 
 // Sizes of an attention call; the tiles of 16 tokens over all heads and
-// sequences are counted in an int32.
+// sequences, and a constant for each, are counted in an int32.
 static qlin_status check_attn(const qlin_kv_desc* d, int32_t q_heads, int32_t B, int32_t max_pages) {
   qlin_status r = check_kv(d);
   if (r != QLIN_OK) return r;
   if (B < 1 || max_pages < 1 || q_heads < 1 || q_heads % d->kv_heads) return QLIN_ERR_SHAPE;
   const int64_t tokens = (int64_t)max_pages * d->page_size;
   if (tokens > 0x7fffffffLL || (int64_t)B * q_heads > 0x7fffffffLL) return QLIN_ERR_SHAPE;
-  if ((double)(tokens / kPageUnit) * (double)B * (double)q_heads > 2147483647.0) return QLIN_ERR_SHAPE;
+  if ((double)(tokens / kPageUnit + kItemExtra) * (double)B * (double)q_heads > 2147483647.0) return QLIN_ERR_SHAPE;
   return QLIN_OK;
 }
 

@@ -437,10 +437,12 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  * s (q - z) of the cache (real numbers, never written), kv head h / (q_heads /
  * kv_heads), x = fp16_rn(R q[b][h]) and R the rotation (R = 1 and x = q[b][h]
  * without sign bits; the codes then are those of unrotated vectors).  Scores,
- * softmax statistics and sums are fp32; the softmax weights enter the product
- * with the values as fp16 (times the token's scale), in numerator and
- * denominator alike.  Deterministic.
- *   q     : device fp16, sequence b's heads [q_heads][head_dim] at element offset
+ * softmax statistics and sums are fp32.  For 4- and 8-bit keys x enters the scores
+ * as 16-bit integers with one power-of-two scale per group of 128 (exact for values
+ * within a factor 8 of the group's largest, others rounded at 2^-14 of it, far
+ * below half a step of the keys); the softmax weights enter the value sums with 22
+ * bits.  Deterministic.
+   q     : device fp16, sequence b's heads [q_heads][head_dim] at element offset
  *           b * q_stride; q_stride >= q_heads * head_dim, a multiple of 8;
  *           q_heads a multiple of kv_heads;
  *   block_table : device int32 [B][max_pages] (4-byte aligned), the page of each

@@ -144,13 +144,15 @@ class Cache:
 def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
     """(out, tolerance) [B, q_heads, dim] in float64, before the final rounding to fp16.
 
-    The tolerance bounds what fp32 scores and fp16 softmax weights may do:
-      * a weight enters as fp16 in numerator and denominator alike, one rounding of
-        relative size 2^-11 each: sum p 2^-11 |v - out| (a weight 2^-21 below the
-        largest may be an fp16 subnormal: 2^-32 absolute, added for every token);
+    The tolerance bounds what fp32 scores and 22-bit softmax weights may do:
+      * a weight enters the value sums as two fp16 digits: 2^-21 relative, or 2^-32 of
+        the largest for every token (digits that are subnormal);
       * a score is 128 or 256 products summed in fp32 (a rounding of 2^-24 of the
-        magnitudes per step, sums of code products and of the zero's share apart):
-        its error e enters as p e |v - out|, twice that with the exponential's own;
+        magnitudes per step, sums of code products and of the zero's share apart);
+      * for 4- and 8-bit keys x is rounded to 16-bit integers of unit 2^(E-13), E the
+        exponent of the group's largest |x|: at most 2^-14 max|x| a value, that is
+        2^-14 max|x| sum |k| a score;
+        a score's error e enters as p e |v - out|, twice that with the exponential's own;
       * the value sums are len products in fp32 over s (q + |z|);
       * everything else (rotation, quotient, joins) is some 64 fp32 steps.
     The inverse rotation mixes a group's errors with weights 1/sqrt(128)."""
@@ -182,11 +184,14 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
             kh, vh = k[:, h // g], v[:, h // g]
             s = scale * (kh @ x)
             e = abs(scale) * (mag[0][:, h // g] @ np.abs(x)) * (D + 64) * 2.0 ** -24 + np.abs(s) * 2.0 ** -22
+            if coded:
+                for c in range(0, D, GROUP):
+                    e = e + abs(scale) * 2.0 ** -14 * np.abs(x[c:c + GROUP]).max() * np.abs(kh[:, c:c + GROUP]).sum(1)
             p = np.exp(s - s.max())
             p /= p.sum()
             o = p @ vh
             far = np.abs(vh - o)
-            d = (p * (2.0 ** -11 + 2 * e + 2.0 ** -20)) @ far + 2.0 ** -32 * far.sum(0)
+            d = (p * (2 * e + 2.0 ** -20)) @ far + 2.0 ** -32 * far.sum(0)
             d = d + (t.size + 64) * 2.0 ** -24 * (p @ mag[1][:, h // g]) + 2.0 ** -18 * np.abs(o)
             out[b, h] = R.T @ o
             tol[b, h] = np.abs(R.T) @ d
