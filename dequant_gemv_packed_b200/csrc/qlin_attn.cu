@@ -37,17 +37,21 @@
 // all tiles of one.  Items in order, each its tiles plus a constant for what an item
 // costs beside them, are cut into equal shares, one a team of warps, whatever the
 // lengths (which only the device knows).  If some item has more than kWholeTiles
-// tiles, the eight (or four) warps of a CTA are a team and items are cut; the pieces
-// go to the workspace (at most two a team: its first and last) and a dependent
-// kernel joins them in order.  Otherwise items stay whole and a team has as few
-// warps as keep all teams busy, down to one: nothing is joined, no barrier is
-// needed.  A team's warps take every T-th tile of its piece, each with its own
-// statistics, joined in shared memory.
+// tiles, the eight (or four) warps of a CTA are a team and items are cut; each team
+// writes its piece of a cut item to the workspace (at most two: its first and last)
+// and the team of an item's first piece a record of it, and a dependent kernel joins
+// the pieces in order, a block a query.  (The last team to arrive joining them by
+// itself was measured slower: one CTA then reads them all, 6 us of 24 at 1 x 32773
+// tokens.)  Otherwise items stay whole and a team has as few warps as keep all teams
+// busy, down to one: nothing is joined, no barrier is needed.  A team's warps take
+// every T-th tile of its piece, each with its own statistics, joined in shared memory.
 //
 // A tile is brought in by its warp alone: 16-byte asynchronous copies into the
 // warp's own ring of stages, swizzled so that both the K reads (rows g, g + 8,
 // 16 bytes a lane) and the transposed V reads (rows 2t, 2t + 1, 2t + 8, 2t + 9)
-// are free of bank conflicts; no barrier is needed but the warp's.
+// are free of bank conflicts; no barrier is needed but the warp's.  The copies run
+// ahead across items, so the stream does not pause where one is finished; its sums
+// pass through the ring's one free stage.
 #include <atomic>
 
 #include "qlin_kv.cuh"
@@ -65,8 +69,12 @@ constexpr int kSms = 148;
 constexpr float kNone = -1e30f;   // running maximum of a warp that has seen no token
 constexpr int kWholeTiles = 32;   // items up to here are not cut
 constexpr int kMinShare = 16;     // tiles a team when they are
-constexpr int kExtra = 2;          // an item's cost beside its tiles, in tiles of one warp
+constexpr int kExtraWarp = 8, kExtraTeam = 24;  // an item's cost beside its tiles, in tiles of a warp alone, of a team
+// A warp's sums in shared memory: 16 values every 20 floats, which spreads both the lanes that
+// write (16 dimensions of a query each) and those that read over the banks.
+constexpr int kDumpRow = 8 * 20 + 8;  // of a query
 constexpr int kMaxTeams = 3 * kSms;  // teams when items are cut: one a CTA
+constexpr int kRecordBytes = kMaxTeams * 16;  // of the workspace: the item that each team is the first to cut
 
 template <int KB, int VB, int NG, int NT>
 struct Cfg {
@@ -74,25 +82,26 @@ struct Cfg {
   static constexpr int kRowK = 16 * KB * NG, kRowV = 16 * VB * NG;  // bytes a token
   static constexpr int kPar = KB == 16 ? 0 : 8 * NG;
   static constexpr int kOffV = kTile * kRowK, kOffPar = kOffV + kTile * kRowV;
-  static constexpr int kStage = kOffPar + kTile * kPar + 16;  // and a word: the tile's tokens
+  static constexpr int kRowQ = 4 * NT;                  // queries
+  static constexpr int kTileBytes = kOffPar + kTile * kPar, kDump = 4 * kDumpRow * 4;
+  // and a word: the tile's tokens; multiples of the longest row, so that swizzles apply to addresses
+  static constexpr int kAlign = KB == 16 ? 256 : 128;
+  static constexpr int kStage = ((kTileBytes > kDump ? kTileBytes : kDump) + 16 + kAlign - 1) / kAlign * kAlign;
   // 32 accumulators a warp (one group, four queries) leave room for 16 warps an SM at 128
   // registers; 64 for 12 at 168, 128 for 8 at 255.  16-bit rows fill the rings: 8 warps.
   static constexpr int kSets = NG * NT;
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
-  static constexpr int kRowQ = 4 * NT;                          // queries
   static constexpr int kSmemQ = kWarps * NT * NG * 1024;        // operand of the queries, a team
   static constexpr int kSmemX = kWarps * kRowQ * NG * 8;        // (scale, sum) of each, a team
-  static constexpr int kSmemMl = kWarps * kRowQ * NG * 8;       // (m, l), a warp
-  static constexpr int kOther = kSmemQ + kSmemX + kSmemMl;
-  static constexpr int fit(int ctas) { return (226 * 1024 / ctas - 1024 - kOther) / (kWarps * kStage); }
+  static constexpr int kSmemMl = kWarps * 4 * 8;                // (m, l) of four queries, a warp
+  static constexpr int kOther = kSmemQ + kSmemX + kSmemMl + kAlign;  // and room to align it
+  static constexpr int fit(int ctas) { return (226 * 1024 / ctas - 4096 - kOther) / (kWarps * kStage); }
   static constexpr int kCtas = kSets == 2 && KB < 16 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;  // per SM
   static constexpr int kStages = fit(kCtas) > 6 ? 6 : fit(kCtas);
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kSmem = kRing + kOther;
   static constexpr int kGrid = kSms * kCtas;
-  static constexpr int kDumpRow = kDim + 8;  // floats; over the warp's idle ring
   static_assert(kStages >= 2, "a stage to fill and one to read");
-  static_assert(kRowQ * kDumpRow * 4 <= kStages * kStage, "sums fit the ring");
 };
 
 struct AttnArgs {
@@ -102,19 +111,25 @@ struct AttnArgs {
   const int32_t *table, *lens;
   const uint32_t* sign_bits;
   __half* out;
+  int4* records;  // [teams] (first output row, queries, last team, -) of the item that a team begins and cuts; 0 queries: none
   float* ws;  // [teams][2] slots of [qper][dim + 4]: sums, then maximum and denominator per group
   float scale_log2e;
   int32_t q_heads, max_pages, batch, cap;  // cap: tokens the table can hold
-  int32_t items, nqb, qper;                // (head, query block) pairs of a sequence; blocks; queries a block
+  int32_t group, items, nqb, qper;  // queries a kv head;             // (head, query block) pairs of a sequence; blocks; queries a block
+  int32_t page_shift;                      // log2 of a page's tiles; -1: no power of two
   int32_t may_cut;                         // the table has room for more than kWholeTiles tiles
 };
 
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, int b) {
-  const int n = min(max(a.lens[b], 0), a.cap);
-  return (n + kTile - 1) / kTile;
-}
+constexpr int kLensCached = 512;
 
-// How the items are dealt out; the same in every warp of both kernels.
+// Tokens and tiles of sequence b; `lens` holds the first kLensCached of a block's.
+__device__ __forceinline__ int clamp_len(const AttnArgs& a, int n) { return min(max(n, 0), a.cap); }
+__device__ __forceinline__ int len_of(const AttnArgs& a, const int* lens, int b) {
+  return b < kLensCached ? lens[b] : clamp_len(a, a.lens[b]);
+}
+__device__ __forceinline__ int tiles_in(int n) { return (n + kTile - 1) / kTile; }
+
+// How the items are dealt out; the same in every warp.
 struct Plan {
   int cut;    // whether items are cut
   int lt;     // log2 of a team's warps
@@ -122,23 +137,36 @@ struct Plan {
   int total, share;
 };
 
-__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int lane, int grid, int warps) {
+template <int kThreads>
+__device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid) {
+  __shared__ int part[3][kThreads / 32];
+  const int lane = threadIdx.x & 31;
+  constexpr int warps = kThreads / 32;
   int n = 0, top = 0, live = 0;
-  for (int b = lane; b < a.batch; b += 32) {
-    const int t = tiles_of(a, b);
+#pragma unroll 2
+  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+    const int len = clamp_len(a, a.lens[b]), t = tiles_in(len);
+    if (b < kLensCached) lens[b] = len;
     n += t;
     top = max(top, t);
     live += t > 0;
   }
   n = __reduce_add_sync(0xffffffffu, n);
   top = __reduce_max_sync(0xffffffffu, top);
-  live = __reduce_add_sync(0xffffffffu, live) * a.items;
+  live = __reduce_add_sync(0xffffffffu, live);
+  if (lane == 0) part[0][threadIdx.x >> 5] = n, part[1][threadIdx.x >> 5] = top, part[2][threadIdx.x >> 5] = live;
+  __syncthreads();
+  n = top = live = 0;
+#pragma unroll
+  for (int i = 0; i < warps; ++i) n += part[0][i], top = max(top, part[1][i]), live += part[2][i];
+  live *= a.items;
   Plan p;
   p.cut = a.may_cut && top > kWholeTiles;
   p.lt = 31 - __clz(warps);
   if (!p.cut)
     while (p.lt > 0 && live > grid * (warps >> p.lt)) --p.lt;
-  p.extra = min(kExtra << p.lt, kItemExtra);
+  p.extra = p.lt ? kExtraTeam : kExtraWarp;
+  static_assert(kExtraWarp <= kItemExtra && kExtraTeam <= kItemExtra, "positions are counted in an int");
   p.total = n * a.items + live * p.extra;
   const int teams = grid * (warps >> p.lt);
   p.share = (int)(((int64_t)p.total + teams - 1) / teams);
@@ -147,10 +175,11 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int lane, int grid,
 }
 
 // The sequence that position u (< total) belongs to, and its first position.
-__device__ __forceinline__ void find_pos(const AttnArgs& a, const Plan& p, int lane, int u, int& b, int& first) {
+__device__ __forceinline__ void find_pos(const AttnArgs& a, const Plan& p, const int* lens, int lane, int u,
+                                         int& b, int& first) {
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int t = b0 + lane < a.batch ? tiles_of(a, b0 + lane) : 0;
+    const int t = b0 + lane < a.batch ? tiles_in(len_of(a, lens, b0 + lane)) : 0;
     const int n = t ? (t + p.extra) * a.items : 0;
     int sum = n;
 #pragma unroll
@@ -246,23 +275,71 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// n / d for 0 <= n < 2^31, d > 0: two estimates in fp32 (the second of a remainder below 2^9 d),
+// each at most one off, and a correction; shorter than the integer division.
+__device__ __forceinline__ int div_pos(int n, int d) {
+  const float r = rcp((float)d) * 0.9999995f;  // from below
+  int q = (int)((float)n * r);
+  int rest = n - q * d;
+  const int more = (int)((float)rest * r);
+  q += more;
+  rest -= more * d;
+  return q + (rest >= d);
+}
+
+// A team's piece of one item.
+struct Segment {
+  int b, hq0, nq, h;  // sequence, first query head and how many, kv head
+  int tile0, n, nt;   // tiles [tile0, tile0 + n) of nt
+  int len, from;      // tokens of the sequence; position of the item's first tile
+};
+
+// A team's place in its share: position, sequence, the sequence's first position and tiles.
+__device__ __forceinline__ bool next_segment(const AttnArgs& a, const Plan& p, const int* lens, int4& cur, int end,
+                                             Segment& s) {
+  int u = cur.x, b = cur.y, first = cur.z, nt = cur.w;
+  while (u < end) {
+    while (nt == 0 || u - first >= (nt + p.extra) * a.items) {  // the next sequence that has tokens
+      if (nt) first += (nt + p.extra) * a.items;
+      ++b;
+      nt = tiles_in(len_of(a, lens, b));
+    }
+    const int cost = nt + p.extra, item = div_pos(u - first, cost), at = (u - first) - item * cost;
+    const int until = p.cut ? min(cost, at + end - u) : cost;
+    u += until - at;
+    s.tile0 = max(at - p.extra, 0);
+    s.n = max(until - p.extra, 0) - s.tile0;
+    if (s.n <= 0) continue;
+    s.b = b, s.nt = nt;
+    s.len = len_of(a, lens, b);
+    s.h = a.nqb == 1 ? item : div_pos(item, a.nqb);
+    const int q0 = (item - s.h * a.nqb) * a.qper;
+    s.nq = min(a.qper, a.group - q0);
+    s.hq0 = s.h * a.group + q0;
+    s.from = first + item * cost + p.extra;
+    cur = make_int4(u, b, first, nt);
+    return true;
+  }
+  return false;
+}
+
 // Byte offset of 16-byte piece c (of a group's row) of tile row r, for the K reads:
 // eight lanes read pieces t, t + 4, ... of rows 2j and 2j + 1.
 template <int KB>
-__device__ __forceinline__ int k_at(int r, int c) {
+__host__ __device__ constexpr int k_at(int r, int c) {
   return r * 16 * KB + 16 * (KB == 4 ? c : c ^ ((r & 1) << 2));
 }
 // The same for the V reads: 4 bits, 16 lanes read 8 bytes of pieces 0, 1 (or 2, 3)
 // of rows 2t; 8 bits, 8 lanes read pieces 2i, 2i + 1 of rows 2t; 16 bits, one piece
 // of eight consecutive rows.
 template <int VB>
-__device__ __forceinline__ int v_at(int r, int c) {
+__host__ __device__ constexpr int v_at(int r, int c) {
   if (VB == 4) return (r >> 1) * 128 + ((r ^ (r >> 1)) & 1) * 64 + 16 * (c ^ ((r >> 1) & 2));
   if (VB == 8) return r * 128 + 16 * (c ^ (r & 6));
   return r * 256 + 16 * (c ^ (r & 7));
 }
 
-// Rotation (or its inverse) of the four values 4 lane .. 4 lane + 3 of block g.
+// Rotation (or its inverse) of the four values 4 lane .. 4 lane + 3 of group g on a warp.
 __device__ __forceinline__ void rotate4(float (&v)[4], const uint32_t* sign_bits, int g, int lane, bool inverse) {
   const uint32_t sw = sign_bits[g * 4 + (lane >> 3)] >> (4 * (lane & 7));
   if (!inverse)
@@ -278,9 +355,8 @@ __device__ __forceinline__ void rotate4(float (&v)[4], const uint32_t* sign_bits
       if ((sw >> i) & 1u) v[i] = -v[i];
 }
 
-// One head's finished sums, group g: four values a lane, rotated back and stored.
-__device__ __forceinline__ void store_out(const AttnArgs& a, int b, int hq, int dim, int g, int lane, float (&r)[4],
-                                          float den) {
+// One group of one head's finished sums on a warp: rotated back and stored.
+__device__ __forceinline__ void store_out4(const AttnArgs& a, int row, int dim, int g, int lane, float (&r)[4], float den) {
   const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] *= inv;
@@ -289,69 +365,146 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int hq, int 
   uint2 w;
   w.x = *reinterpret_cast<const uint32_t*>(&h0);
   w.y = *reinterpret_cast<const uint32_t*>(&h1);
-  *reinterpret_cast<uint2*>(a.out + ((int64_t)b * a.q_heads + hq) * dim + g * kGroup + 4 * lane) = w;
+  *reinterpret_cast<uint2*>(a.out + (int64_t)row * dim + g * kGroup + 4 * lane) = w;
 }
 
-// Prepares query `q` of a team (rotation, fp16, digits or halves) in its shared operand.
+// One group of one head's finished sums on eight lanes: rotated back and stored.
+__device__ __forceinline__ void store_out(const AttnArgs& a, bool live, int row, int dim, int g, int t,
+                                          float (&r)[16], float den) {
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] *= inv;
+  if (a.sign_bits) {
+    fwht128_oct(r, t);
+    flip16(r, a.sign_bits[g * 4 + (t >> 1)] >> (16 * (t & 1)));
+  }
+  uint4 h0, h1;
+  float_to_halves(r, h0, h1);
+  if (!live) return;
+  uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)row * dim + g * kGroup) + 2 * t;
+  out[0] = h0, out[1] = h1;
+}
+
+// Prepares group g of a query (rotation, fp16, digits or halves) in its team's shared
+// operand, eight lanes a group (lane t: dimensions 16 t .. 16 t + 15 of it).
 //   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim], at 4
 //   bits the dimensions of each eight in the order 0 2 4 6 1 3 5 7 (a word's even codes, its odd).
 template <int KB, int NG>
-__device__ __forceinline__ void prepare_query(const AttnArgs& a, const __half* src, bool live, int q, int lane,
-                                              uint8_t* sq, float2* sx) {
+__device__ __forceinline__ void prepare_query(const AttnArgs& a, uint4 r0, uint4 r1, int q, int g, int t, uint8_t* sq,
+                                              float2* sx) {
   constexpr int D = NG * kGroup;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-      const uint2 r = *reinterpret_cast<const uint2*>(src + g * kGroup + 4 * lane);
-      const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
-      const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
-      v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
-      if (a.sign_bits) rotate4(v, a.sign_bits, g, lane, false);
-    }
-    const __half2 h0 = __floats2half2_rn(v[0], v[1]), h1 = __floats2half2_rn(v[2], v[3]);
-    if (KB == 16) {
-      uint2 w;
-      w.x = *reinterpret_cast<const uint32_t*>(&h0);
-      w.y = *reinterpret_cast<const uint32_t*>(&h1);
-      *reinterpret_cast<uint2*>(sq + (q * D + g * kGroup + 4 * lane) * 2) = w;
-      if (lane == 0) sx[q * NG + g] = make_float2(a.scale_log2e, 0.f);
-      continue;
-    }
-    v[0] = __low2float(h0), v[1] = __high2float(h0), v[2] = __low2float(h1), v[3] = __high2float(h1);
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
-    big = __reduce_max_sync(0xffffffffu, big);
-    const int e = (int)(big >> 23) - 127;  // exponent of the largest (a half is a normal float, or 0)
-    const float down = __uint_as_float((uint32_t)(127 + 13 - e) << 23), up = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-    int xi[4], sum = 0;
-    uint32_t hi = 0, lo = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      xi[i] = big ? __float2int_rn(v[i] * down) : 0;
-      sum += xi[i];
-      const int l = ((xi[i] + 128) & 255) - 128;
-      hi |= (uint32_t)(((xi[i] - l) >> 8) & 255) << (8 * i);
-      lo |= (uint32_t)(l & 255) << (8 * i);
-    }
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    uint8_t* row = sq + (2 * q) * D + g * kGroup;
-    if (KB == 8) {
-      *reinterpret_cast<uint32_t*>(row + 4 * lane) = hi;
-      *reinterpret_cast<uint32_t*>(row + D + 4 * lane) = lo;
-    } else {  // dimensions 4l .. 4l+3 of an eight: its bytes 2 (l & 1), + 1 (even) and 4 bytes on (odd)
-      row += 8 * (lane >> 1) + 2 * (lane & 1);
-      *reinterpret_cast<uint16_t*>(row) = (uint16_t)__byte_perm(hi, 0, 0x4420);
-      *reinterpret_cast<uint16_t*>(row + 4) = (uint16_t)__byte_perm(hi, 0, 0x4431);
-      *reinterpret_cast<uint16_t*>(row + D) = (uint16_t)__byte_perm(lo, 0, 0x4420);
-      *reinterpret_cast<uint16_t*>(row + D + 4) = (uint16_t)__byte_perm(lo, 0, 0x4431);
-    }
-    // the sums of 4-bit codes are kept times 16; a query with an infinity or NaN has no scale
-    const float unit = KB == 4 ? 0.0625f : 1.f;
-    const float f = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : big ? a.scale_log2e * up * unit : 0.f;
-    if (lane == 0) sx[q * NG + g] = make_float2(f, (float)sum / unit);
+  float v[16];
+  if (a.sign_bits) {
+    halves_to_float(r0, r1, v);
+    flip16(v, a.sign_bits[g * 4 + (t >> 1)] >> (16 * (t & 1)));
+    fwht128_oct(v, t);
+    float_to_halves(v, r0, r1);
   }
+  if (KB == 16) {
+    uint4* dst = reinterpret_cast<uint4*>(sq + (q * D + g * kGroup) * 2) + 2 * t;
+    dst[0] = r0, dst[1] = r1;
+    if (t == 0) sx[q * NG + g] = make_float2(a.scale_log2e, 0.f);
+    return;
+  }
+  halves_to_float(r0, r1, v);
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+  const int e = (int)(big >> 23) - 127;  // exponent of the largest (a half is a normal float, or 0)
+  const float down = big ? __uint_as_float((uint32_t)(127 + 13 - e) << 23) : 0.f;
+  uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int xi = __float2int_rn(v[i] * down), up = xi + 128;  // xi = 256 (up >> 8) + (up & 255) - 128
+    sum += xi;
+    // 4 bits: bytes 0 2 4 6 of an eight, then 1 3 5 7
+    const int at = KB == 8 ? i : (i & 8) + ((i & 1) << 2) + ((i & 7) >> 1);
+    hi[at >> 2] |= (uint32_t)((up >> 8) & 255) << (8 * (at & 3));
+    lo[at >> 2] |= (uint32_t)((up & 255) ^ 128) << (8 * (at & 3));
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  uint8_t* row = sq + (2 * q) * D + g * kGroup + 16 * t;
+  *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(row + D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  // the sums of 4-bit codes are kept times 16; a query with an infinity or NaN has no scale
+  const float unit = KB == 4 ? 0.0625f : 1.f, step = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+  const float f = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : big ? a.scale_log2e * step * unit : 0.f;
+  if (t == 0) sx[q * NG + g] = make_float2(f, (float)sum / unit);
+}
+
+// Sums of query j, dimensions 4 lane .. 4 lane + 3 of a group, over a team's warps.
+__device__ __forceinline__ void gather4(const uint8_t* smem, const int* dump_at, const float2* sml, int T, int j,
+                                        int lane, float (&r)[4], float& top, float& den) {
+  top = kNone, den = 0.f;
+  r[0] = r[1] = r[2] = r[3] = 0.f;
+  for (int w = 0; w < T; ++w) top = fmaxf(top, sml[w * 4 + j].x);
+#pragma unroll 4
+  for (int w = 0; w < T; ++w) {
+    const float2 ml = sml[w * 4 + j];
+    const float f = ex2(ml.x - top);
+    const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + dump_at[w]) + j * kDumpRow +
+                                                      20 * (lane >> 2) + 4 * (lane & 3));
+    den = fmaf(f, ml.y, den);
+    r[0] = fmaf(f, v.x, r[0]), r[1] = fmaf(f, v.y, r[1]), r[2] = fmaf(f, v.z, r[2]), r[3] = fmaf(f, v.w, r[3]);
+  }
+}
+
+// The same on a whole warp (lane: dimensions 4 lane .. 4 lane + 3): shorter, for teams that have a
+// warp for each query.
+template <int KB, int NG>
+__device__ __forceinline__ void prepare_query4(const AttnArgs& a, uint2 r, int q, int g, int lane, uint8_t* sq,
+                                               float2* sx) {
+  constexpr int D = NG * kGroup;
+  float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+  float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+  float v[4] = {f0.x, f0.y, f1.x, f1.y};
+  if (a.sign_bits) {
+    rotate4(v, a.sign_bits, g, lane, false);
+    const __half2 h0 = __floats2half2_rn(v[0], v[1]), h1 = __floats2half2_rn(v[2], v[3]);
+    r.x = *reinterpret_cast<const uint32_t*>(&h0);
+    r.y = *reinterpret_cast<const uint32_t*>(&h1);
+    f0 = __half22float2(h0), f1 = __half22float2(h1);
+    v[0] = f0.x, v[1] = f0.y, v[2] = f1.x, v[3] = f1.y;
+  }
+  if (KB == 16) {
+    *reinterpret_cast<uint2*>(sq + (q * D + g * kGroup + 4 * lane) * 2) = r;
+    if (lane == 0) sx[q * NG + g] = make_float2(a.scale_log2e, 0.f);
+    return;
+  }
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
+  big = __reduce_max_sync(0xffffffffu, big);
+  const int e = (int)(big >> 23) - 127;
+  const float down = big ? __uint_as_float((uint32_t)(127 + 13 - e) << 23) : 0.f;
+  int sum = 0;
+  uint32_t hi = 0, lo = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int xi = __float2int_rn(v[i] * down), up = xi + 128;
+    sum += xi;
+    hi |= (uint32_t)((up >> 8) & 255) << (8 * i);
+    lo |= (uint32_t)((up & 255) ^ 128) << (8 * i);
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  uint8_t* row = sq + (2 * q) * D + g * kGroup;
+  if (KB == 8) {
+    *reinterpret_cast<uint32_t*>(row + 4 * lane) = hi;
+    *reinterpret_cast<uint32_t*>(row + D + 4 * lane) = lo;
+  } else {  // dimensions 4l .. 4l+3 of an eight: its bytes 2 (l & 1), + 1 (even) and 4 bytes on (odd)
+    row += 8 * (lane >> 1) + 2 * (lane & 1);
+    *reinterpret_cast<uint16_t*>(row) = (uint16_t)__byte_perm(hi, 0, 0x4420);
+    *reinterpret_cast<uint16_t*>(row + 4) = (uint16_t)__byte_perm(hi, 0, 0x4431);
+    *reinterpret_cast<uint16_t*>(row + D) = (uint16_t)__byte_perm(lo, 0, 0x4420);
+    *reinterpret_cast<uint16_t*>(row + D + 4) = (uint16_t)__byte_perm(lo, 0, 0x4431);
+  }
+  const float unit = KB == 4 ? 0.0625f : 1.f, step = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+  const float f = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : big ? a.scale_log2e * step * unit : 0.f;
+  if (lane == 0) sx[q * NG + g] = make_float2(f, (float)sum / unit);
 }
 
 template <int KB, int VB, int NG, int NT>
@@ -359,28 +512,21 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     attn_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<KB, VB, NG, NT>;
   constexpr int NW = C::kWarps, S = C::kStages, D = C::kDim;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_addr(smem_raw) & (C::kAlign - 1u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const int grid = gridDim.x, page_tiles = a.c.page / kTile;
   uint8_t* const ring_ptr = smem + warp * S * C::kStage;
   const uint32_t ring = smem_addr(ring_ptr);
 
   if (a.may_cut && threadIdx.x == 0) grid_launch_dependents();
-  // sequences without tokens
-  for (int b = blockIdx.x; b < a.batch; b += grid) {
-    const int n = a.lens[b];
-    if (n > a.cap && threadIdx.x == 0) atomicOr(&g_attn_error, kKvBadLength);
-    if (n <= 0)
-      for (int i = threadIdx.x; i < a.q_heads * D / 8; i += NW * 32)
-        reinterpret_cast<uint4*>(a.out + (int64_t)b * a.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-
-  const Plan plan = make_plan(a, lane, grid, NW);
+  __shared__ int lens[kLensCached];
+  const Plan plan = make_plan<NW * 32>(a, lens, grid);
   const int lt = plan.lt, T = 1 << lt, team = warp >> lt, tw = warp & (T - 1);
   const int teams = NW >> lt, worker = blockIdx.x * teams + team;
   uint8_t* sq = smem + C::kRing + team * (NT * NG * 1024);
   float2* sx = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ) + team * C::kRowQ * NG;
-  float2* sml = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ + C::kSmemX) + (warp - tw) * C::kRowQ * NG;
+  float2* sml = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ + C::kSmemX) + (warp - tw) * 4;
   auto team_barrier = [&]() {
     if (lt)
       named_barrier(1 + team, 32 << lt);
@@ -389,88 +535,142 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   };
 
   const int64_t begin = (int64_t)worker * plan.share;
-  if (begin >= plan.total) return;
-  int u = (int)begin;
   const int end = (int)min((int64_t)plan.total, begin + plan.share);
-  int b, first;
-  find_pos(a, plan, lane, u, b, first);
-  int nt = tiles_of(a, b), cost = nt + plan.extra;
-  if (!plan.cut && (u - first) % cost) u += cost - (u - first) % cost;  // items that start in the share
-  const int group = a.q_heads / a.c.heads;
-  while (u < end) {
-    while (nt == 0 || u - first >= cost * a.items) {  // the next sequence that has tokens
-      if (nt) first += cost * a.items;
-      ++b;
-      nt = tiles_of(a, b);
-      cost = nt + plan.extra;
+  __shared__ int4 place[NW][2];      // a warp's places: of its copies, of its sums
+  __shared__ int dump_at[NW];        // where a warp's sums are, in bytes
+  int4 record = make_int4(0, 0, 0, 0);
+  bool more = begin < plan.total;
+  Segment seg = {};
+  if (more) {
+    int4 cur = make_int4((int)begin, 0, 0, 0);
+    find_pos(a, plan, lens, lane, cur.x, cur.y, cur.z);
+    cur.w = tiles_in(len_of(a, lens, cur.y));
+    if (!plan.cut) {  // items that start in the share
+      const int cost = cur.w + plan.extra, at = (cur.x - cur.z) % cost;
+      if (at) cur.x += cost - at;
     }
-    const int item = (u - first) / cost, at = (u - first) % cost;
-    const int until = plan.cut ? min(cost, at + end - u) : cost;
-    u += until - at;
-    const int tile0 = max(at - plan.extra, 0), n = max(until - plan.extra, 0) - tile0;
-    if (n <= 0) continue;
-    const int len = min(a.lens[b], a.cap);
-    const int h = item / a.nqb, q0 = (item % a.nqb) * a.qper;
-    const int nq = min(a.qper, group - q0);
-    const int hq0 = h * group + q0;
-
-    // ---- the warp's tiles: tile0 + tw + T k, k < cnt; pages of 32 of them in registers
-    const int cnt = tw < n ? (n - tw + T - 1) >> lt : 0;
-    int pages = 0, offs = 0;
-    auto issue = [&](int k) {
-      if (k < cnt) {
-        if ((k & 31) == 0) {
-          const int kk = k + lane;
-          pages = -1;
-          if (kk < cnt) {
-            const int tile = tile0 + tw + (kk << lt);
-            pages = a.table[(int64_t)b * a.max_pages + tile / page_tiles];
-            offs = (tile % page_tiles) * kTile;
-          }
-        }
-        int p = __shfl_sync(0xffffffffu, pages, k & 31);
-        const int off = __shfl_sync(0xffffffffu, offs, k & 31);
-        int valid = min(kTile, len - (tile0 + tw + (k << lt)) * kTile);
-        if ((unsigned)p >= (unsigned)a.c.pages) {
-          if (lane == 0) atomicOr(&g_attn_error, kKvBadPage);
-          p = 0;
-          valid = 0;
-        }
-        const int stage = (k % S) * C::kStage;
-        const uint32_t st = ring + stage;
-        const uint8_t* blk = a.c.block(p, h);
-        const uint8_t* src = blk + (int64_t)off * C::kRowK + 16 * lane;
-#pragma unroll
-        for (int j = 0; j < KB * NG / 2; ++j) {
-          const int i = lane + 32 * j, r = i / (KB * NG), c = i % (KB * NG);
-          cp16(st + (c / KB) * (kTile * 16 * KB) + k_at<KB>(r, c % KB), src + 512 * j);
-        }
-        src = blk + a.c.v_offset() + (int64_t)off * C::kRowV + 16 * lane;
-#pragma unroll
-        for (int j = 0; j < VB * NG / 2; ++j) {
-          const int i = lane + 32 * j, r = i / (VB * NG), c = i % (VB * NG);
-          const uint32_t dst = st + C::kOffV + (c / VB) * (kTile * 16 * VB) + v_at<VB>(r, c % VB);
-          // 16-bit values past the length could be NaN, which a weight of zero would not hide
-          if (VB == 16)
-            cp16_or_zero(dst, src + 512 * j, r < valid);
-          else
-            cp16(dst, src + 512 * j);
-        }
-        if (C::kPar) {
-          if (lane < kTile * C::kPar / 16)
-            cp16(st + C::kOffPar + 16 * lane, blk + a.c.par_offset() + (int64_t)off * C::kPar + 16 * lane);
-        }
-        if (lane == 0) *reinterpret_cast<int*>(ring_ptr + stage + C::kStage - 16) = valid;
+    more = next_segment(a, plan, lens, cur, end, seg);
+    if (lane == 0) place[warp][0] = place[warp][1] = cur;
+  }
+  bool have = more;
+  // the warp's part of a segment's queries: a (query, group) on the warp if the team has a warp for
+  // each of four, else four of them on eight lanes each
+  uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
+  auto load_query = [&](int i) {
+    const int j = lt >= 2 ? i : 4 * i + (lane >> 3), q = j / NG;
+    q0 = q1 = make_uint4(0u, 0u, 0u, 0u);
+    if (q < seg.nq) {
+      const __half* src = a.q + (int64_t)seg.b * a.q_stride + (int64_t)(seg.hq0 + q) * D + (j % NG) * kGroup;
+      if (lt >= 2) {
+        const uint2 r = reinterpret_cast<const uint2*>(src)[lane];
+        q0.x = r.x, q0.y = r.y;
+      } else {
+        q0 = reinterpret_cast<const uint4*>(src)[2 * (lane & 7)];
+        q1 = reinterpret_cast<const uint4*>(src)[2 * (lane & 7) + 1];
       }
-      cp_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < S - 1; ++k) issue(k);
+    }
+  };
+  if (have) load_query(tw);
 
+  // ---- copies: tile ik of icnt of the warp's piece of the segment that they have reached
+  int ik = 0, icnt = have && tw < seg.n ? (seg.n - tw + T - 1) >> lt : 0;
+  int itile = seg.tile0 + tw, ilen = seg.len, ih = seg.h, istage = 0;
+  uint32_t src_lo = 0, src_hi = 0, meta = 0;  // of 32 tiles, one a lane: address of the K rows; offset in the page, tokens
+  // where the lane's first piece goes; piece j goes to (first ^ swizzle(j)) + pitch(j), a constant each
+  constexpr int RK = KB * NG, RV = VB * NG;
+  const uint32_t k_dst = ring + (lane % RK) / KB * (kTile * 16 * KB) + k_at<KB>(lane / RK, lane % KB);
+  const uint32_t v_dst = ring + C::kOffV + (lane % RV) / VB * (kTile * 16 * VB) + v_at<VB>(lane / RV, lane % VB);
+  const int32_t* itable = a.table + (int64_t)seg.b * a.max_pages;
+  __syncwarp();
+  auto issue = [&]() {
+    while (more && ik >= icnt) {
+      int4 cur = place[warp][0];
+      __syncwarp();
+      Segment s;
+      more = next_segment(a, plan, lens, cur, end, s);
+      if (more) {
+        if (lane == 0) place[warp][0] = cur;
+        __syncwarp();
+        ik = 0;
+        icnt = tw < s.n ? (s.n - tw + T - 1) >> lt : 0;
+        itile = s.tile0 + tw;
+        ilen = s.len;
+        ih = s.h;
+        itable = a.table + (int64_t)s.b * a.max_pages;
+      }
+    }
+    if (more) {
+      if ((ik & 31) == 0) {
+        const int kk = ik + lane;
+        if (kk < icnt) {
+          const int tile = itile + (kk << lt), page = a.page_shift >= 0 ? tile >> a.page_shift : tile / page_tiles;
+          int p = itable[page], valid = min(kTile, ilen - tile * kTile);
+          if ((unsigned)p >= (unsigned)a.c.pages) {
+            atomicOr(&g_attn_error, kKvBadPage);
+            p = 0;
+            valid = 0;
+          }
+          const int off = (tile - page * page_tiles) * kTile;
+          const uint64_t src = reinterpret_cast<uint64_t>(a.c.block(p, ih)) + (int64_t)off * C::kRowK;
+          src_lo = (uint32_t)src, src_hi = (uint32_t)(src >> 32);
+          meta = (uint32_t)off << 5 | (uint32_t)valid;
+        }
+      }
+      const uint32_t lo = __shfl_sync(0xffffffffu, src_lo, ik & 31), hi = __shfl_sync(0xffffffffu, src_hi, ik & 31);
+      const uint32_t mt = __shfl_sync(0xffffffffu, meta, ik & 31), valid = mt & 31u, off = mt >> 5;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo) + 16 * lane;
+      const uint32_t at = istage * C::kStage;
+#pragma unroll
+      for (int j = 0; j < RK / 2; ++j) {
+        constexpr int pitch = 16 * KB;
+        const int r = 32 * j / RK;
+        cp16(((k_dst + at) ^ (uint32_t)(k_at<KB>(r, 0) - r * pitch)) + r * pitch, src + 512 * j);
+      }
+      const uint8_t* v_src = src + a.c.v_offset();
+      if (RV != RK) v_src += (int64_t)((int)off * (C::kRowV - C::kRowK));
+#pragma unroll
+      for (int j = 0; j < RV / 2; ++j) {
+        constexpr int pitch = 16 * VB;
+        const int r = 32 * j / RV;
+        const uint32_t dst = ((v_dst + at) ^ (uint32_t)(v_at<VB>(r, 0) - r * pitch)) + r * pitch;
+        // 16-bit values past the length could be NaN, which a weight of zero would not hide
+        if (VB == 16)
+          cp16_or_zero(dst, v_src + 512 * j, (unsigned)(lane / RV + r) < valid);
+        else
+          cp16(dst, v_src + 512 * j);
+      }
+      if (C::kPar) {
+        if (lane < kTile * C::kPar / 16)
+          cp16(ring + at + C::kOffPar + 16 * lane, src + a.c.par_offset() + (int64_t)((int)off * (C::kPar - C::kRowK)));
+      }
+      if (lane == 0) *reinterpret_cast<uint32_t*>(ring_ptr + at + C::kStage - 16) = valid;
+      ++ik;
+      istage = istage + 1 == S ? 0 : istage + 1;
+    }
+    cp_commit();
+  };
+#pragma unroll 1
+  for (int k = 0; k < S - 1; ++k) issue();
+
+  int stage_no = 0;  // of the tile to be read next
+  const uint32_t k_src = ring + k_at<KB>(g8, t4);  // rows g8 and g8 + 8, pieces t4, t4 + 4 (at ^ 64), ...
+  const uint32_t v_src = ring + C::kOffV +
+                         (VB == 4   ? v_at<VB>(2 * t4, g8 >> 1) + 8 * (g8 & 1)
+                          : VB == 8 ? v_at<VB>(2 * t4, g8)
+                                    : v_at<VB>((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1));
+  while (have) {
+    const int cnt = tw < seg.n ? (seg.n - tw + T - 1) >> lt : 0;
     // ---- the queries, and the lane's operand: column g8 = (query g8 / 2, digit g8 % 2), the
     // dimensions of the codes that lanes of column t4 hold
-    for (int q = tw; q < C::kRowQ; q += T)
-      prepare_query<KB, NG>(a, a.q + (int64_t)b * a.q_stride + (int64_t)(hq0 + q) * D, q < nq, q, lane, sq, sx);
+    for (int i = tw; i < (lt >= 2 ? C::kRowQ * NG : NT * NG); i += T) {
+      if (i != tw) load_query(i);
+      if (lt >= 2) {
+        prepare_query4<KB, NG>(a, make_uint2(q0.x, q0.y), i / NG, i % NG, lane, sq, sx);
+      } else {
+        const int j = 4 * i + (lane >> 3);
+        prepare_query<KB, NG>(a, q0, q1, j / NG, j % NG, lane & 7, sq, sx);
+      }
+    }
     team_barrier();
     constexpr int NB = KB == 16 ? 16 : 8;  // operand registers a group
     uint32_t qf[NT][NG][NB];
@@ -511,8 +711,9 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     for (int k = 0; k < cnt; ++k) {
       cp_wait<S - 2>();
       __syncwarp();
-      issue(k + S - 1);  // into the stage that the previous tile has left
-      const int stage = (k % S) * C::kStage;
+      issue();  // into the stage that the previous tile has left
+      const int stage = stage_no * C::kStage;
+      stage_no = stage_no + 1 == S ? 0 : stage_no + 1;
       const uint32_t st = ring + stage;
       const int valid = *reinterpret_cast<const volatile int*>(ring_ptr + stage + C::kStage - 16);
 
@@ -524,9 +725,9 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float dot[NT][2];
-        const uint32_t kb = st + g * (kTile * 16 * KB);
+        const uint32_t kb = k_src + stage + g * (kTile * 16 * KB);
         if (KB == 4) {
-          const uint4 wa = ld128(kb + k_at<KB>(g8, t4)), wb = ld128(kb + k_at<KB>(g8 + 8, t4));
+          const uint4 wa = ld128(kb), wb = ld128(kb + 128 * KB);
           const uint32_t ra[4] = {wa.x, wa.y, wa.z, wa.w}, rb[4] = {wb.x, wb.y, wb.z, wb.w};
           int c0[NT][4], c1[NT][4];
 #pragma unroll
@@ -556,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             for (int i = 0; i < 4; ++i) c0[s][i] = c1[s][i] = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint4 wa = ld128(kb + k_at<KB>(g8, t4 + 4 * j)), wb = ld128(kb + k_at<KB>(g8 + 8, t4 + 4 * j));
+            const uint4 wa = ld128(kb ^ (64 * j)), wb = ld128((kb ^ (64 * j)) + 128 * KB);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
               imma(c0[s], wa.x, wb.x, wa.y, wb.y, qf[s][g][4 * j], qf[s][g][4 * j + 1]);
@@ -576,7 +777,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             for (int i = 0; i < 4; ++i) c0[s][i] = c1[s][i] = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 wa = ld128(kb + k_at<KB>(g8, t4 + 4 * j)), wb = ld128(kb + k_at<KB>(g8 + 8, t4 + 4 * j));
+            const uint4 wa = ld128(kb ^ (64 * j)), wb = ld128((kb ^ (64 * j)) + 128 * KB);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
               mma(c0[s], wa.x, wb.x, wa.y, wb.y, qf[s][g][(4 * j) % NB], qf[s][g][(4 * j + 1) % NB]);
@@ -652,11 +853,11 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
       // values: the lane's tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, dimensions 16 g8 .. 16 g8 + 15
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint32_t vb = st + C::kOffV + g * (kTile * 16 * VB);
+        const uint32_t vb = v_src + stage + g * (kTile * 16 * VB);
         if (VB == 4) {
           uint2 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = ld64(vb + v_at<VB>(2 * t4 + (i & 1) + 8 * (i >> 1), g8 >> 1) + 8 * (g8 & 1));
+          for (int i = 0; i < 4; ++i) v[i] = ld64((vb ^ (64 * (i & 1))) + 512 * (i >> 1));
 #pragma unroll
           for (int half = 0; half < 4; ++half) {  // four dimensions: a half-word of each token
             const uint32_t sel = (half & 1) ? 0x7632u : 0x5410u;
@@ -673,7 +874,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         } else if (VB == 8) {
           uint4 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = ld128(vb + v_at<VB>(2 * t4 + (i & 1) + 8 * (i >> 1), g8));
+          for (int i = 0; i < 4; ++i) v[i] = ld128(vb + 128 * (i & 1) + 1024 * (i >> 1));
           const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
           const uint32_t v2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
@@ -685,20 +886,24 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             for (int s = 0; s < NT; ++s) mma(o[s][g][j], x0, x1, y0, y1, pb[s][g][0], pb[s][g][1]);
           }
         } else {
-          const int r = (lane & 7) + 8 * (lane >> 4), c = (lane >> 3) & 1;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint4 v = ldmatrix_x4_trans(vb + v_at<VB>(r, 2 * j + c));
+            const uint4 v = ldmatrix_x4_trans(vb ^ (32 * j));
 #pragma unroll
             for (int s = 0; s < NT; ++s) mma(o[s][g][j], v.x, v.y, v.z, v.w, pb[s][g][0], pb[s][g][1]);
           }
         }
       }
     }
-    cp_wait<0>();
-    __syncwarp();  // the warp has left its ring
+    __syncwarp();  // every lane has read the last tile, and its stage is free
 
-    // ---- the warp's sums [query][dim] over its ring, then the team's
+    // ---- the sums of four queries and one group at a time: each warp's into its free stage, then the
+    // team's
+    float* dump = reinterpret_cast<float*>(ring_ptr + istage * C::kStage);
+    if (lane == 0) dump_at[warp] = warp * S * C::kStage + istage * C::kStage;
+    const int slot = seg.tile0 == 0;  // 0: the item began in an earlier share
+    if (seg.n != seg.nt && slot)
+      record = make_int4(seg.b * a.q_heads + seg.hq0, seg.nq, (seg.from + seg.nt - 1) / plan.share, 0);
 #pragma unroll
     for (int s = 0; s < NT; ++s)
 #pragma unroll
@@ -708,123 +913,148 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           l[s][g] += __shfl_xor_sync(0xffffffffu, l[s][g], d);
           zc[s][g] += __shfl_xor_sync(0xffffffffu, zc[s][g], d);
         }
-        float* row = reinterpret_cast<float*>(ring_ptr) + (4 * s + t4) * C::kDumpRow + g * kGroup;
+        float* row = dump + t4 * kDumpRow;
 #pragma unroll
         for (int j = 0; j < 8; j += (VB == 16 ? 1 : 2)) {
           const float(&e)[4] = o[s][g][j];
           const float e0 = fmaf(e[1], 0x1p-11f, e[0]), e1 = fmaf(e[3], 0x1p-11f, e[2]);
           if (VB == 16) {
-            row[16 * j + g8] = e0, row[16 * j + 8 + g8] = e1;
+            row[20 * j + g8] = e0, row[20 * j + 8 + g8] = e1;
           } else {
             const float(&f)[4] = o[s][g][(j + 1) & 7];
             const float f0 = fmaf(f[1], 0x1p-11f, f[0]), f1 = fmaf(f[3], 0x1p-11f, f[2]), z = -zc[s][g];
             const float r0 = fmaf(e0, 512.f, z), r1 = fmaf(e1, 512.f, z), r2 = fmaf(f0, 512.f, z), r3 = fmaf(f1, 512.f, z);
             // 4 bits: rows (0, 2) and (1, 3) of four dimensions; 8 bits: (0, 1) and (2, 3)
-            *reinterpret_cast<float4*>(row + 16 * g8 + 2 * j) =
+            *reinterpret_cast<float4*>(row + 20 * g8 + 2 * j) =
                 VB == 4 ? make_float4(r0, r2, r1, r3) : make_float4(r0, r1, r2, r3);
           }
         }
-        if (g8 == 0) sml[(tw * C::kRowQ + 4 * s + t4) * NG + g] = make_float2(m[s][g], l[s][g]);
-      }
-    team_barrier();
-    const bool whole = n == nt;
-    for (int q = tw; q < nq; q += T)
+        if (g8 == 0) sml[tw * 4 + t4] = make_float2(m[s][g], l[s][g]);
+        team_barrier();
+        if (lt >= 2) {
+          for (int j = tw; j < 4; j += T)
+            if (4 * s + j < seg.nq) {
+              float r[4], top, den;
+              gather4(smem, dump_at + warp - tw, sml, T, j, lane, r, top, den);
+              if (seg.n == seg.nt) {
+                store_out4(a, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, lane, r, den);
+              } else {
+                float* to = a.ws + (((int64_t)worker * 2 + slot) * a.qper + 4 * s + j) * (D + 4);
+                __stcg(reinterpret_cast<float4*>(to + g * kGroup + 4 * lane), make_float4(r[0], r[1], r[2], r[3]));
+                if (lane == 0) __stcg(reinterpret_cast<float2*>(to + D + 2 * g), make_float2(top, den));
+              }
+            }
+        } else if (tw == 0) {  // four queries on eight lanes each
+          const int j = lane >> 3, c8 = lane & 7;
+          float top = kNone, den = 0.f, r[16];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float top = kNone, den = 0.f, r[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < T; ++i) top = fmaxf(top, sml[(i * C::kRowQ + q) * NG + g].x);
-        for (int i = 0; i < T; ++i) {
-          const float2 ml = sml[(i * C::kRowQ + q) * NG + g];
-          const float f = ex2(ml.x - top);
-          const float4 v = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(smem + (warp - tw + i) * S * C::kStage) + q * C::kDumpRow + g * kGroup +
-              4 * lane);
-          den = fmaf(f, ml.y, den);
-          r[0] = fmaf(f, v.x, r[0]), r[1] = fmaf(f, v.y, r[1]), r[2] = fmaf(f, v.z, r[2]), r[3] = fmaf(f, v.w, r[3]);
+          for (int c = 0; c < 16; ++c) r[c] = 0.f;
+          for (int w = 0; w < T; ++w) top = fmaxf(top, sml[w * 4 + j].x);
+          for (int w = 0; w < T; ++w) {
+            const float2 ml = sml[w * 4 + j];
+            const float f = ex2(ml.x - top);
+            const float4* from = reinterpret_cast<const float4*>(
+                reinterpret_cast<const float*>(smem + dump_at[warp - tw + w]) + j * kDumpRow + 20 * c8);
+            den = fmaf(f, ml.y, den);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float4 v = from[c];
+              r[4 * c] = fmaf(f, v.x, r[4 * c]), r[4 * c + 1] = fmaf(f, v.y, r[4 * c + 1]);
+              r[4 * c + 2] = fmaf(f, v.z, r[4 * c + 2]), r[4 * c + 3] = fmaf(f, v.w, r[4 * c + 3]);
+            }
+          }
+          store_out(a, 4 * s + j < seg.nq, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, c8, r, den);
         }
-        if (whole) {
-          store_out(a, b, hq0 + q, D, g, lane, r, den);
-        } else {  // slot 0: the item began in an earlier team's share; slot 1: here
-          float* slot = a.ws + ((int64_t)worker * 2 + (tile0 == 0)) * a.qper * (D + 4) + q * (D + 4);
-          *reinterpret_cast<float4*>(slot + g * kGroup + 4 * lane) = make_float4(r[0], r[1], r[2], r[3]);
-          if (lane == 0) slot[D + 2 * g] = top, slot[D + 2 * g + 1] = den;
-        }
+        team_barrier();  // the stage, the statistics and the queries may be overwritten
       }
-    team_barrier();  // rings and queries may be overwritten
+
+    int4 cur = place[warp][1];
+    __syncwarp();
+    have = next_segment(a, plan, lens, cur, end, seg);
+    if (lane == 0) place[warp][1] = cur;
+    __syncwarp();
+    if (have) load_query(tw);
   }
+  cp_wait<0>();
+
+  // sequences without tokens
+  for (int b = blockIdx.x; b < a.batch; b += grid) {
+    const int n = a.lens[b];
+    if (n > a.cap && threadIdx.x == 0) atomicOr(&g_attn_error, kKvBadLength);
+    if (n <= 0)
+      for (int i = threadIdx.x; i < a.q_heads * D / 8; i += NW * 32)
+        reinterpret_cast<uint4*>(a.out + (int64_t)b * a.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  if (a.may_cut && threadIdx.x == 0) a.records[blockIdx.x] = record;  // items are cut: a team is the CTA
 }
 
-// Joins the pieces of the item that is cut between shares blockIdx.x and
-// blockIdx.x + 1, if no earlier cut is inside it; one query a block, four warps over
-// its pieces.
+// Joins the pieces of the item that team blockIdx.x begins and cuts, if there is one; a query
+// (blockIdx.y) a block, kJoinWarps warps over its pieces.
+constexpr int kJoinWarps = 8;
+
 template <int NG>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a, int grid, int warps) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int D = NG * kGroup;
-  __shared__ float so[4][D], sm[4][NG], sl[4][NG];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Plan plan = make_plan(a, lane, grid, warps);
-  const int64_t cut64 = (int64_t)(blockIdx.x + 1) * plan.share;
-  bool mine = plan.cut && cut64 < plan.total;
-  const int cut = (int)cut64, group = a.q_heads / a.c.heads, q = blockIdx.y;
-  int b = 0, h = 0, q0 = 0, last = 0;
-  if (mine) {
-    int first = 0;
-    find_pos(a, plan, lane, cut, b, first);
-    const int nt = tiles_of(a, b), cost = nt + plan.extra, item = (cut - first) / cost;
-    const int from = first + item * cost + plan.extra;  // position of the item's first tile
-    last = from + nt - 1;
-    h = item / a.nqb, q0 = (item % a.nqb) * a.qper;
-    // inside the tiles, and the first cut there
-    mine = cut > from && cut - plan.share <= from && q < min(a.qper, group - q0);
-  }
+  __shared__ __align__(16) float sums[NG][kJoinWarps][kGroup];
+  __shared__ float2 sml[NG][kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = blockIdx.y, c0 = blockIdx.x;
   grid_dependency_wait();  // every block: this grid's end stands for the first one's too
-  if (!mine) return;
-  const int c0 = blockIdx.x, c1 = last / plan.share;  // its teams
+  const int4 rec = __ldcg(a.records + c0);
+  if (q >= rec.y) return;
   float top[NG], den[NG], r[NG][4];
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    top[g] = kNone, den[g] = 0.f;
-    r[g][0] = r[g][1] = r[g][2] = r[g][3] = 0.f;
-  }
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const float* slot = a.ws + ((int64_t)c * 2 + (c == c0)) * a.qper * (D + 4) + q * (D + 4);
+  for (int g = 0; g < NG; ++g) top[g] = kNone, den[g] = r[g][0] = r[g][1] = r[g][2] = r[g][3] = 0.f;
+  for (int c = c0 + warp; c <= rec.z; c += 4 * kJoinWarps) {  // four pieces at a time
+    float4 v[4][NG];
+    float2 ml[4][NG];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const float2 ml = *reinterpret_cast<const float2*>(slot + D + 2 * g);
-      const float4 v = *reinterpret_cast<const float4*>(slot + g * kGroup + 4 * lane);
-      const float n = fmaxf(top[g], ml.x), f = ex2(top[g] - n), e = ex2(ml.x - n);
-      top[g] = n;
-      den[g] = den[g] * f + e * ml.y;
-      r[g][0] = r[g][0] * f + e * v.x, r[g][1] = r[g][1] * f + e * v.y;
-      r[g][2] = r[g][2] * f + e * v.z, r[g][3] = r[g][3] * f + e * v.w;
+    for (int i = 0; i < 4; ++i) {
+      const int k = c + i * kJoinWarps;
+      const float* p = a.ws + (((int64_t)k * 2 + (k == c0)) * a.qper + q) * (D + 4);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const bool live = k <= rec.z;
+        ml[i][g] = live ? __ldcg(reinterpret_cast<const float2*>(p + D + 2 * g)) : make_float2(kNone, 0.f);
+        v[i][g] = live ? __ldcg(reinterpret_cast<const float4*>(p + g * kGroup + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float next = fmaxf(top[g], ml[i][g].x), f = ex2(top[g] - next), e = ex2(ml[i][g].x - next);
+        top[g] = next;
+        den[g] = den[g] * f + e * ml[i][g].y;
+        r[g][0] = r[g][0] * f + e * v[i][g].x, r[g][1] = r[g][1] * f + e * v[i][g].y;
+        r[g][2] = r[g][2] * f + e * v[i][g].z, r[g][3] = r[g][3] * f + e * v[i][g].w;
+      }
   }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    *reinterpret_cast<float4*>(&so[warp][g * kGroup + 4 * lane]) = make_float4(r[g][0], r[g][1], r[g][2], r[g][3]);
-    if (lane == 0) sm[warp][g] = top[g], sl[warp][g] = den[g];
+    *reinterpret_cast<float4*>(&sums[g][warp][4 * lane]) = make_float4(r[g][0], r[g][1], r[g][2], r[g][3]);
+    if (lane == 0) sml[g][warp] = make_float2(top[g], den[g]);
   }
   __syncthreads();
   if (warp >= NG) return;
-  const int g = warp;
   float t = kNone, d = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int w = 0; w < 4; ++w) t = fmaxf(t, sm[w][g]);
+  for (int w = 0; w < kJoinWarps; ++w) t = fmaxf(t, sml[warp][w].x);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ex2(sm[w][g] - t);
-    d = fmaf(f, sl[w][g], d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fmaf(f, so[w][g * kGroup + 4 * lane + i], v[i]);
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float2 ml = sml[warp][w];
+    const float f = ex2(ml.x - t);
+    const float4 s = *reinterpret_cast<const float4*>(&sums[warp][w][4 * lane]);
+    d = fmaf(f, ml.y, d);
+    v[0] = fmaf(f, s.x, v[0]), v[1] = fmaf(f, s.y, v[1]), v[2] = fmaf(f, s.z, v[2]), v[3] = fmaf(f, s.w, v[3]);
   }
-  store_out(a, b, h * group + q0 + q, D, g, lane, v, d);
+  store_out4(a, rec.x + q, D, warp, lane, v, d);
 }
 
 template <int KB, int VB, int NG, int NT>
 qlin_status launch(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<KB, VB, NG, NT>;
-  static_assert(C::kSmem <= 227 * 1024 && C::kGrid <= kMaxTeams, "launch bounds");
+  static_assert(C::kSmem <= 226 * 1024 && C::kGrid <= kMaxTeams, "launch bounds");
   static std::atomic<unsigned long long> configured{0};  // per-device attribute, set once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -839,14 +1069,14 @@ qlin_status launch(const AttnArgs& a, cudaStream_t s) {
   if (r != QLIN_OK || !a.may_cut) return r;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C::kGrid - 1, a.qper);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return record_cuda(cudaLaunchKernelEx(&cfg, attn_join_kernel<NG>, a, (int)C::kGrid, (int)C::kWarps));
+  return record_cuda(cudaLaunchKernelEx(&cfg, attn_join_kernel<NG>, a));
 }
 
 template <int NG, int NT>
@@ -881,7 +1111,7 @@ unsigned take_attn_error() {
 size_t attn_workspace_bytes(const qlin_kv_desc* d, int q_heads, int, int max_pages) {
   const Split s = split_of(d->page_size, d->kv_heads, q_heads, max_pages);
   if (!s.may_cut) return 0;
-  return (size_t)kMaxTeams * 2 * s.qper * (d->head_dim + 4) * sizeof(float);
+  return kRecordBytes + (size_t)kMaxTeams * 2 * s.qper * (d->head_dim + 4) * sizeof(float);
 }
 
 qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_stride, int q_heads,
@@ -896,12 +1126,16 @@ qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_strid
   a.lens = seq_lens;
   a.sign_bits = sign_bits;
   a.out = out;
-  a.ws = static_cast<float*>(workspace);
+  a.records = static_cast<int4*>(workspace);
+  a.ws = sp.may_cut ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes) : nullptr;
+  const int page_tiles = c.page / kTile;
+  a.page_shift = page_tiles & (page_tiles - 1) ? -1 : __builtin_ctz(page_tiles);
   a.scale_log2e = scale * kLog2e;
   a.q_heads = q_heads;
   a.max_pages = max_pages;
   a.batch = batch;
   a.cap = max_pages * c.page;
+  a.group = q_heads / c.heads;
   a.items = c.heads * sp.nqb;
   a.nqb = sp.nqb;
   a.qper = sp.qper;

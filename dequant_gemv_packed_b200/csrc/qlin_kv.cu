@@ -37,57 +37,6 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return d;
 }
 
-// Butterflies of strides 1..64 over the 16 values of each of a group's eight lanes.
-__device__ __forceinline__ void fwht128_oct(float (&v)[16], int t) {
-#pragma unroll
-  for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (!(j & h)) {
-        const float a = v[j], b = v[j + h];
-        v[j] = __fadd_rn(a, b);
-        v[j + h] = __fsub_rn(a, b);
-      }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    const bool upper = (t & o) != 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float p = __shfl_xor_sync(0xffffffffu, v[j], o);
-      v[j] = upper ? __fsub_rn(p, v[j]) : __fadd_rn(v[j], p);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], kInvSqrt128);
-}
-
-__device__ __forceinline__ void flip16(float (&v)[16], uint32_t sw) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    v[j] = __uint_as_float(__float_as_uint(v[j]) ^ (((sw >> j) & 1u) << 31));
-}
-
-__device__ __forceinline__ void halves_to_float(const uint4& r0, const uint4& r1, float (&v)[16]) {
-  const uint32_t raw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
-__device__ __forceinline__ void float_to_halves(const float (&v)[16], uint4& r0, uint4& r1) {
-  uint32_t raw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    raw[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  r0 = make_uint4(raw[0], raw[1], raw[2], raw[3]);
-  r1 = make_uint4(raw[4], raw[5], raw[6], raw[7]);
-}
-
 struct KvArgs {
   KvView c;
   const __half *k_in, *v_in;  // write: token rows
