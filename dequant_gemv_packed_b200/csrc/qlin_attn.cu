@@ -269,24 +269,6 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// n / d for 0 <= n < 2^31, d > 0: two estimates in fp32 (the second of a remainder below 2^9 d),
-// each at most one off, and a correction; shorter than the integer division.
-__device__ __forceinline__ int div_pos(int n, int d) {
-  const float r = rcp((float)d) * 0.9999995f;  // from below
-  int q = (int)((float)n * r);
-  int rest = n - q * d;
-  const int more = (int)((float)rest * r);
-  q += more;
-  rest -= more * d;
-  return q + (rest >= d);
-}
-
 // A team's piece of one item.
 struct Segment {
   int b, hq0, nq, h;  // sequence, first query head and how many, kv head
@@ -356,11 +338,12 @@ __device__ __forceinline__ void rotate4(float (&v)[4], const uint32_t* sign_bits
 }
 
 // One group of one head's finished sums on a warp: rotated back and stored.
-__device__ __forceinline__ void store_out4(const AttnArgs& a, int row, int dim, int g, int lane, float (&r)[4], float den) {
+__device__ __forceinline__ void store_out4(const AttnArgs& a, const uint32_t* signs, int row, int dim, int g, int lane,
+                                           float (&r)[4], float den) {
   const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] *= inv;
-  if (a.sign_bits) rotate4(r, a.sign_bits, g, lane, true);
+  if (a.sign_bits) rotate4(r, signs, g, lane, true);
   const __half2 h0 = __floats2half2_rn(r[0], r[1]), h1 = __floats2half2_rn(r[2], r[3]);
   uint2 w;
   w.x = *reinterpret_cast<const uint32_t*>(&h0);
@@ -369,14 +352,14 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, int row, int dim, 
 }
 
 // One group of one head's finished sums on eight lanes: rotated back and stored.
-__device__ __forceinline__ void store_out(const AttnArgs& a, bool live, int row, int dim, int g, int t,
+__device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* signs, bool live, int row, int dim, int g, int t,
                                           float (&r)[16], float den) {
   const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
   for (int i = 0; i < 16; ++i) r[i] *= inv;
   if (a.sign_bits) {
     fwht128_oct(r, t);
-    flip16(r, a.sign_bits[g * 4 + (t >> 1)] >> (16 * (t & 1)));
+    flip16(r, signs[g * 4 + (t >> 1)] >> (16 * (t & 1)));
   }
   uint4 h0, h1;
   float_to_halves(r, h0, h1);
@@ -390,13 +373,13 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, bool live, int row,
 //   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim], at 4
 //   bits the dimensions of each eight in the order 0 2 4 6 1 3 5 7 (a word's even codes, its odd).
 template <int KB, int NG>
-__device__ __forceinline__ void prepare_query(const AttnArgs& a, uint4 r0, uint4 r1, int q, int g, int t, uint8_t* sq,
+__device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t* signs, uint4 r0, uint4 r1, int q, int g, int t, uint8_t* sq,
                                               float2* sx) {
   constexpr int D = NG * kGroup;
   float v[16];
   if (a.sign_bits) {
     halves_to_float(r0, r1, v);
-    flip16(v, a.sign_bits[g * 4 + (t >> 1)] >> (16 * (t & 1)));
+    flip16(v, signs[g * 4 + (t >> 1)] >> (16 * (t & 1)));
     fwht128_oct(v, t);
     float_to_halves(v, r0, r1);
   }
@@ -456,14 +439,14 @@ __device__ __forceinline__ void gather4(const uint8_t* smem, const int* dump_at,
 // The same on a whole warp (lane: dimensions 4 lane .. 4 lane + 3): shorter, for teams that have a
 // warp for each query.
 template <int KB, int NG>
-__device__ __forceinline__ void prepare_query4(const AttnArgs& a, uint2 r, int q, int g, int lane, uint8_t* sq,
+__device__ __forceinline__ void prepare_query4(const AttnArgs& a, const uint32_t* signs, uint2 r, int q, int g, int lane, uint8_t* sq,
                                                float2* sx) {
   constexpr int D = NG * kGroup;
   float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
   float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
   float v[4] = {f0.x, f0.y, f1.x, f1.y};
   if (a.sign_bits) {
-    rotate4(v, a.sign_bits, g, lane, false);
+    rotate4(v, signs, g, lane, false);
     const __half2 h0 = __floats2half2_rn(v[0], v[1]), h1 = __floats2half2_rn(v[2], v[3]);
     r.x = *reinterpret_cast<const uint32_t*>(&h0);
     r.y = *reinterpret_cast<const uint32_t*>(&h1);
@@ -521,6 +504,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 
   if (a.may_cut && threadIdx.x == 0) grid_launch_dependents();
   __shared__ int lens[kLensCached];
+  __shared__ uint32_t signs[4 * NG];
+  if (a.sign_bits && threadIdx.x < 4 * NG) signs[threadIdx.x] = a.sign_bits[threadIdx.x];
   const Plan plan = make_plan<NW * 32>(a, lens, grid);
   const int lt = plan.lt, T = 1 << lt, team = warp >> lt, tw = warp & (T - 1);
   const int teams = NW >> lt, worker = blockIdx.x * teams + team;
@@ -665,10 +650,10 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     for (int i = tw; i < (lt >= 2 ? C::kRowQ * NG : NT * NG); i += T) {
       if (i != tw) load_query(i);
       if (lt >= 2) {
-        prepare_query4<KB, NG>(a, make_uint2(q0.x, q0.y), i / NG, i % NG, lane, sq, sx);
+        prepare_query4<KB, NG>(a, signs, make_uint2(q0.x, q0.y), i / NG, i % NG, lane, sq, sx);
       } else {
         const int j = 4 * i + (lane >> 3);
-        prepare_query<KB, NG>(a, q0, q1, j / NG, j % NG, lane & 7, sq, sx);
+        prepare_query<KB, NG>(a, signs, q0, q1, j / NG, j % NG, lane & 7, sq, sx);
       }
     }
     team_barrier();
@@ -937,7 +922,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
               float r[4], top, den;
               gather4(smem, dump_at + warp - tw, sml, T, j, lane, r, top, den);
               if (seg.n == seg.nt) {
-                store_out4(a, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, lane, r, den);
+                store_out4(a, signs, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, lane, r, den);
               } else {
                 float* to = a.ws + (((int64_t)worker * 2 + slot) * a.qper + 4 * s + j) * (D + 4);
                 __stcg(reinterpret_cast<float4*>(to + g * kGroup + 4 * lane), make_float4(r[0], r[1], r[2], r[3]));
@@ -963,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
               r[4 * c + 2] = fmaf(f, v.z, r[4 * c + 2]), r[4 * c + 3] = fmaf(f, v.w, r[4 * c + 3]);
             }
           }
-          store_out(a, 4 * s + j < seg.nq, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, c8, r, den);
+          store_out(a, signs, 4 * s + j < seg.nq, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, c8, r, den);
         }
         team_barrier();  // the stage, the statistics and the queries may be overwritten
       }
@@ -1048,7 +1033,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     d = fmaf(f, ml.y, d);
     v[0] = fmaf(f, s.x, v[0]), v[1] = fmaf(f, s.y, v[1]), v[2] = fmaf(f, s.z, v[2]), v[3] = fmaf(f, s.w, v[3]);
   }
-  store_out4(a, rec.x + q, D, warp, lane, v, d);
+  store_out4(a, a.sign_bits, rec.x + q, D, warp, lane, v, d);
 }
 
 template <int KB, int VB, int NG, int NT>

@@ -15,7 +15,11 @@
 // 64, so the stored bytes are a function of the input alone.
 //
 // Eight lanes a group, 16 consecutive values each: strides 1 to 8 in the lane,
-// 16 to 64 over lane distances 1, 2, 4.
+// 16 to 64 over lane distances 1, 2, 4.  The quotients v / s share one correctly
+// rounded reciprocal r and take three multiply-adds each, q0 = v r,
+// q0 + (v - q0 s) r: correctly rounded by Markstein's theorem (IBM Journal of
+// Research and Development 34, 1990), s having 11 significant bits and nothing
+// here nearing the ends of the exponent range.
 #include "qlin_kv.cuh"
 
 namespace qlin {
@@ -58,17 +62,16 @@ struct Task {
 
 __device__ __forceinline__ Task find_task(const KvArgs& a, int t, int64_t stride_k, int64_t stride_v) {
   Task k;
-  const int groups = a.c.dim / kGroup;
-  const int64_t total = (int64_t)a.tokens * a.c.heads * 2 * groups;
-  const int64_t id = (int64_t)blockIdx.x * kTasksPerCta + (threadIdx.x >> 3);
-  k.live = id < total;
-  int64_t i = k.live ? id : total - 1;
-  k.g = (int)(i % groups);
-  i /= groups;
-  k.side = (int)(i & 1);
-  i >>= 1;
-  const int h = (int)(i % a.c.heads);
-  const int tok = (int)(i / a.c.heads);
+  const int lg = a.c.dim == kGroup ? 0 : 1, groups = 1 << lg, unit = a.c.heads * 2 * groups;  // tasks a token
+  // the block's first task by one division, the block's others by a short one
+  const unsigned base = blockIdx.x * (unsigned)kTasksPerCta, tok0 = base / (unsigned)unit;
+  const int x = (int)(base - tok0 * unit) + (int)(threadIdx.x >> 3), ahead = div_pos(x, unit);
+  int tok = (int)tok0 + ahead, r = x - ahead * unit;
+  k.live = tok < a.tokens;
+  if (!k.live) tok = a.tokens - 1, r = 0;
+  k.g = r & (groups - 1);
+  k.side = (r >> lg) & 1;
+  const int h = r >> (lg + 1);
   k.bits = k.side ? a.c.v_bits : a.c.k_bits;
   k.in = (int64_t)tok * (k.side ? stride_v : stride_k) + (int64_t)h * a.c.dim + (int64_t)k.g * kGroup;
   k.slot = a.slots[tok];
@@ -77,10 +80,9 @@ __device__ __forceinline__ Task find_task(const KvArgs& a, int t, int64_t stride
     k.slot = -1;
   }
   const int s = k.slot < 0 ? 0 : k.slot;
-  uint8_t* b = a.c.pool + ((int64_t)(s / a.c.page) * a.c.heads + h) * a.c.block_bytes;
-  const int off = s % a.c.page;
-  k.row = b + (k.side ? a.c.v_offset() + (int64_t)off * a.c.v_row : (int64_t)off * a.c.k_row) +
-          (int64_t)k.g * (kGroup / 8) * k.bits;
+  const int page = a.c.page_shift >= 0 ? s >> a.c.page_shift : s / a.c.page, off = s - page * a.c.page;
+  uint8_t* b = const_cast<uint8_t*>(a.c.block(page, h));
+  k.row = b + (k.side ? a.c.v_offset() + (int64_t)off * a.c.v_row : (int64_t)off * a.c.k_row) + k.g * (kGroup / 8) * k.bits;
   k.par = b + a.c.par_offset() + (int64_t)off * a.c.par + 8 * k.g + 4 * k.side;
   return k;
 }
@@ -127,20 +129,29 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
   // a group that holds an infinity or NaN reads back as NaN throughout
   const __half z16 = finite ? __float2half_rn(__fdiv_rn(-lo, s)) : __ushort_as_half(0x7fff);
   const float z = __half2float(z16);
-  uint32_t q[16];
+  const float inv = __frcp_rn(s);
+  uint32_t q[16];  // the code in the low byte: adding 2^23 rounds to an integer, ties to even
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    q[j] = (uint32_t)fminf(fmaxf(rintf(__fadd_rn(__fdiv_rn(v[j], s), z)), 0.f), qmax);
+  for (int j = 0; j < 16; ++j) {
+    const float q0 = __fmul_rn(v[j], inv), d = __fmaf_rn(__fmaf_rn(-q0, s, v[j]), inv, q0);
+    q[j] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fadd_rn(d, z), 0.f), qmax), 8388608.f));
+  }
   if (!store) return;
   if (k.bits == 8) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = q[4 * i] | q[4 * i + 1] << 8 | q[4 * i + 2] << 16 | q[4 * i + 3] << 24;
+    for (int i = 0; i < 4; ++i)
+      w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
     reinterpret_cast<uint4*>(k.row)[t] = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    uint32_t w[2] = {0u, 0u};
+    uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j >> 3] |= q[j] << (4 * (j & 7));
+    for (int i = 0; i < 2; ++i) {
+      uint32_t b[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) b[c] = q[8 * i + 2 * c] + (q[8 * i + 2 * c + 1] << 4);
+      w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
     reinterpret_cast<uint2*>(k.row)[t] = make_uint2(w[0], w[1]);
   }
   if (t == 0) *reinterpret_cast<__half2*>(k.par) = __halves2half2(s16, z16);
@@ -194,11 +205,11 @@ unsigned take_kv_error() {
   return v;
 }
 
+// Tasks are counted in 31 bits.
 static qlin_status kv_grid(const KvArgs& a, unsigned* grid) {
   const int64_t tasks = (int64_t)a.tokens * a.c.heads * 2 * (a.c.dim / kGroup);
-  const int64_t g = (tasks + kTasksPerCta - 1) / kTasksPerCta;
-  if (g > 0x7fffffffLL) return QLIN_ERR_SHAPE;
-  *grid = (unsigned)g;
+  if (tasks > 0x7fffffffLL - kTasksPerCta) return QLIN_ERR_SHAPE;
+  *grid = (unsigned)((tasks + kTasksPerCta - 1) / kTasksPerCta);
   return QLIN_OK;
 }
 

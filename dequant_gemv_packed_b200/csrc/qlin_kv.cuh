@@ -26,11 +26,11 @@ struct KvView {
   int32_t k_bits, v_bits;
   int32_t k_row, v_row;  // bytes of a row
   int32_t par;           // bytes of a token's parameters (0 at 16 bits)
+  int32_t page_shift;    // log2 of the page's tokens; -1: no power of two
 
   __host__ __device__ const uint8_t* block(int p, int h) const {
     return pool + ((int64_t)p * heads + h) * block_bytes;
   }
-  __host__ __device__ uint8_t* block(int p, int h) { return pool + ((int64_t)p * heads + h) * block_bytes; }
   __host__ __device__ int64_t v_offset() const { return (int64_t)page * k_row; }
   __host__ __device__ int64_t par_offset() const { return (int64_t)page * (k_row + v_row); }
 };
@@ -42,6 +42,7 @@ __host__ inline KvView make_kv_view(const qlin_kv_desc* d, const void* cache) {
   v.page = d->page_size;
   v.heads = d->kv_heads;
   v.dim = d->head_dim;
+  v.page_shift = d->page_size & (d->page_size - 1) ? -1 : __builtin_ctz(d->page_size);
   v.k_bits = d->k_bits;
   v.v_bits = d->v_bits;
   v.k_row = d->head_dim * d->k_bits / 8;
@@ -57,6 +58,24 @@ constexpr unsigned kKvBadPage = 2u;    // a page outside the pool within a seque
 constexpr unsigned kKvBadLength = 4u;  // a length beyond the sequence's row of the block table
 unsigned take_kv_error();              // each file's own word, read and cleared
 unsigned take_attn_error();
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// n / d for 0 <= n < 2^31, d > 0: two estimates in fp32 (the second of a remainder below 2^9 d),
+// each at most one off, and a correction; shorter than the integer division.
+__device__ __forceinline__ int div_pos(int n, int d) {
+  const float r = rcp((float)d) * 0.9999995f;  // from below
+  int q = (int)((float)n * r);
+  int rest = n - q * d;
+  const int more = (int)((float)rest * r);
+  q += more;
+  rest -= more * d;
+  return q + (rest >= d);
+}
 
 // A group of 128 values on eight lanes, lane t = lane % 8 with values 16 t .. 16 t + 15.
 

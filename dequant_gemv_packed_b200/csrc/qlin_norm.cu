@@ -1,46 +1,147 @@
 // qlin_rmsnorm: residual addition and root-mean-square norm in front of a linear
 // layer, y = fp16(h / sqrt(mean h^2 + eps) * weight), h = fp16(x + residual).
 //
-// One CTA a row; bound by HBM (x, residual in; y, residual out).
+// A row stays in registers between its two uses: `warps` warps a row, up to eight
+// 16-byte pieces (64 values) a lane.  Bound by HBM: x and the residual in, y and
+// the residual out, each once.
 #include "qlin_internal.cuh"
 
 namespace qlin {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxWarps = 32;
 
-__global__ void __launch_bounds__(kThreads) rmsnorm_kernel(const __half* __restrict__ x, const __half* residual,
-                                                           const __half* __restrict__ weight, float eps,
-                                                           __half* __restrict__ y, __half* residual_out, int K) {
-  __shared__ float part[kThreads / 32];
-  const int64_t row = (int64_t)blockIdx.x * K;
-  float sum = 0.f;
-  for (int i = threadIdx.x; i < K; i += kThreads) {
-    float h = __half2float(x[row + i]);
-    if (residual) {
-      const __half r = __float2half_rn(h + __half2float(residual[row + i]));
-      residual_out[row + i] = r;
-      h = __half2float(r);
-    }
-    sum += h * h;
+struct NormArgs {
+  const uint4 *x, *residual, *weight;
+  uint4 *y, *residual_out;
+  float eps, inv_k;
+  int rows, pieces;  // of 8 values a row
+};
+
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = p.x, f[2 * i + 1] = p.y;
   }
+}
+
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One row a block (blockDim.y = 1) or a warp (blockDim.x = 32); NP pieces a thread.
+template <int NP, bool kResidual>
+__global__ void __launch_bounds__(kMaxWarps * 32) rmsnorm_kernel(const NormArgs a) {
+  __shared__ float part[kMaxWarps];
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= a.rows) return;  // whole warps: blocks of several rows have one warp each
+  const int64_t base = (int64_t)row * a.pieces;
+  uint4 h[NP], r[NP], w[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int p = threadIdx.x + i * blockDim.x;
+    h[i] = r[i] = w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p < a.pieces) {
+      h[i] = a.x[base + p];
+      if (kResidual) r[i] = a.residual[base + p];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int p = threadIdx.x + i * blockDim.x;
+    if (p < a.pieces) w[i] = __ldg(a.weight + p);
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    float f[8];
+    unpack(h[i], f);
+    if (kResidual) {
+      float g[8];
+      unpack(r[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += g[j];
+      h[i] = pack(f);
+      unpack(h[i], f);
+      const int p = threadIdx.x + i * blockDim.x;
+      if (p < a.pieces) a.residual_out[base + p] = h[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+  }
+#pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = 0.f;
-  for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
-  const float inv = 1.f / sqrtf(sum / (float)K + eps);
-  const __half* h = residual ? residual_out : x;  // each thread reads back what it wrote
-  for (int i = threadIdx.x; i < K; i += kThreads)
-    y[row + i] = __float2half_rn(__half2float(h[row + i]) * inv * __half2float(weight[i]));
+  if (blockDim.x > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  const float scale = 1.f / sqrtf(fmaf(sum, a.inv_k, a.eps));
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int p = threadIdx.x + i * blockDim.x;
+    if (p < a.pieces) {
+      float f[8], g[8];
+      unpack(h[i], f);
+      unpack(w[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * scale * g[j];
+      a.y[base + p] = pack(f);
+    }
+  }
+}
+
+template <bool kResidual>
+qlin_status launch(const NormArgs& a, cudaStream_t s) {
+  // A warp a row up to 1,024 values (four rows a block); longer rows a block, two pieces a thread
+  // (8 lines in flight each) until the block is full.
+  if (a.pieces <= 128) {
+    const dim3 block(32, 4);
+    const unsigned grid = (unsigned)((a.rows + 3) / 4);
+    if (a.pieces <= 32)
+      rmsnorm_kernel<1, kResidual><<<grid, block, 0, s>>>(a);
+    else if (a.pieces <= 64)
+      rmsnorm_kernel<2, kResidual><<<grid, block, 0, s>>>(a);
+    else
+      rmsnorm_kernel<4, kResidual><<<grid, block, 0, s>>>(a);
+    return record_cuda(cudaGetLastError());
+  }
+  const unsigned grid = (unsigned)a.rows;
+  const auto threads = [&](int np) { return dim3((unsigned)(((a.pieces + np - 1) / np + 31) / 32 * 32)); };
+  if (a.pieces <= 2048)
+    rmsnorm_kernel<2, kResidual><<<grid, threads(2), 0, s>>>(a);
+  else if (a.pieces <= 4096)
+    rmsnorm_kernel<4, kResidual><<<grid, threads(4), 0, s>>>(a);
+  else
+    rmsnorm_kernel<8, kResidual><<<grid, threads(8), 0, s>>>(a);
+  return record_cuda(cudaGetLastError());
 }
 
 }  // namespace
 
 qlin_status launch_rmsnorm(const __half* x, const __half* residual, const __half* weight, float eps, __half* y,
                            __half* residual_out, int M, int K, cudaStream_t s) {
-  rmsnorm_kernel<<<M, kThreads, 0, s>>>(x, residual, weight, eps, y, residual_out, K);
-  return record_cuda(cudaGetLastError());
+  NormArgs a;
+  a.x = reinterpret_cast<const uint4*>(x);
+  a.residual = reinterpret_cast<const uint4*>(residual);
+  a.weight = reinterpret_cast<const uint4*>(weight);
+  a.y = reinterpret_cast<uint4*>(y);
+  a.residual_out = reinterpret_cast<uint4*>(residual_out);
+  a.eps = eps;
+  a.inv_k = 1.f / (float)K;
+  a.rows = M;
+  a.pieces = K / 8;
+  return residual ? launch<true>(a, s) : launch<false>(a, s);
 }
 
 }  // namespace qlin
