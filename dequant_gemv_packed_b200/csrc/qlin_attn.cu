@@ -352,44 +352,54 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, const uint32_t* si
 }
 
 // One group of one head's finished sums on eight lanes: rotated back and stored.
-__device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* signs, bool live, int row, int dim, int g, int t,
-                                          float (&r)[16], float den) {
+__device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* signs, bool live, int row, int dim, int g,
+                                          int t, const float (&r)[16], float den) {
   const float inv = den == 0.f ? 0.f : 1.f / den;
+  f32x2 v[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] *= inv;
-  if (a.sign_bits) {
-    fwht128_oct(r, t);
-    flip16(r, signs[g * 4 + (t >> 1)] >> (16 * (t & 1)));
-  }
+  for (int i = 0; i < 8; ++i) v[i] = pair2(r[2 * i] * inv, r[2 * i + 1] * inv);
   uint4 h0, h1;
-  float_to_halves(r, h0, h1);
+  if (a.sign_bits) {
+    uint32_t flip[8];
+    sign_masks(signs + 4 * g, t, flip);
+    fwht128_oct(v, t);
+    float_to_halves(v, h0, h1);
+    flip16(h0, h1, flip);
+  } else {
+    float_to_halves(v, h0, h1);
+  }
   if (!live) return;
-  uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)row * dim + g * kGroup) + 2 * t;
-  out[0] = h0, out[1] = h1;
+  uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)row * dim + g * kGroup) + t;
+  out[0] = h0, out[8] = h1;
 }
 
 // Prepares group g of a query (rotation, fp16, digits or halves) in its team's shared
-// operand, eight lanes a group (lane t: dimensions 16 t .. 16 t + 15 of it).
+// operand, eight lanes a group (lane t: dimensions 8 t .. 8 t + 7 and 64 on).
 //   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim], at 4
 //   bits the dimensions of each eight in the order 0 2 4 6 1 3 5 7 (a word's even codes, its odd).
 template <int KB, int NG>
-__device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t* signs, uint4 r0, uint4 r1, int q, int g, int t, uint8_t* sq,
-                                              float2* sx) {
+__device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t* signs, uint4 r0, uint4 r1, int q, int g,
+                                              int t, uint8_t* sq, float2* sx) {
   constexpr int D = NG * kGroup;
-  float v[16];
+  f32x2 p[8];
   if (a.sign_bits) {
-    halves_to_float(r0, r1, v);
-    flip16(v, signs[g * 4 + (t >> 1)] >> (16 * (t & 1)));
-    fwht128_oct(v, t);
-    float_to_halves(v, r0, r1);
+    uint32_t flip[8];
+    sign_masks(signs + 4 * g, t, flip);
+    flip16(r0, r1, flip);
+    halves_to_float(r0, r1, p);
+    fwht128_oct(p, t);
+    float_to_halves(p, r0, r1);
   }
   if (KB == 16) {
-    uint4* dst = reinterpret_cast<uint4*>(sq + (q * D + g * kGroup) * 2) + 2 * t;
-    dst[0] = r0, dst[1] = r1;
+    uint4* dst = reinterpret_cast<uint4*>(sq + (q * D + g * kGroup) * 2) + t;
+    dst[0] = r0, dst[8] = r1;
     if (t == 0) sx[q * NG + g] = make_float2(a.scale_log2e, 0.f);
     return;
   }
-  halves_to_float(r0, r1, v);
+  halves_to_float(r0, r1, p);
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split2(p[i], v[2 * i], v[2 * i + 1]);
   uint32_t big = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
@@ -410,9 +420,9 @@ __device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t*
   }
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  uint8_t* row = sq + (2 * q) * D + g * kGroup + 16 * t;
-  *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(row + D) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  uint2* row = reinterpret_cast<uint2*>(sq + (2 * q) * D + g * kGroup) + t;
+  row[0] = make_uint2(hi[0], hi[1]), row[8] = make_uint2(hi[2], hi[3]);
+  row[D / 8] = make_uint2(lo[0], lo[1]), row[D / 8 + 8] = make_uint2(lo[2], lo[3]);
   // the sums of 4-bit codes are kept times 16; a query with an infinity or NaN has no scale
   const float unit = KB == 4 ? 0.0625f : 1.f, step = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
   const float f = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : big ? a.scale_log2e * step * unit : 0.f;
@@ -550,8 +560,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         const uint2 r = reinterpret_cast<const uint2*>(src)[lane];
         q0.x = r.x, q0.y = r.y;
       } else {
-        q0 = reinterpret_cast<const uint4*>(src)[2 * (lane & 7)];
-        q1 = reinterpret_cast<const uint4*>(src)[2 * (lane & 7) + 1];
+        q0 = reinterpret_cast<const uint4*>(src)[lane & 7];
+        q1 = reinterpret_cast<const uint4*>(src)[(lane & 7) + 8];
       }
     }
   };
@@ -611,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         const int r = 32 * j / RK;
         cp16(((k_dst + at) ^ (uint32_t)(k_at<KB>(r, 0) - r * pitch)) + r * pitch, src + 512 * j);
       }
-      const uint8_t* v_src = src + a.c.v_offset();
+      const uint8_t* v_src = src + a.c.v_offset;
       if (RV != RK) v_src += (int64_t)((int)off * (C::kRowV - C::kRowK));
 #pragma unroll
       for (int j = 0; j < RV / 2; ++j) {
@@ -626,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
       }
       if (C::kPar) {
         if (lane < kTile * C::kPar / 16)
-          cp16(ring + at + C::kOffPar + 16 * lane, src + a.c.par_offset() + (int64_t)((int)off * (C::kPar - C::kRowK)));
+          cp16(ring + at + C::kOffPar + 16 * lane, src + a.c.par_offset + (int64_t)((int)off * (C::kPar - C::kRowK)));
       }
       if (lane == 0) *reinterpret_cast<uint32_t*>(ring_ptr + at + C::kStage - 16) = valid;
       ++ik;
@@ -939,11 +949,12 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const float2 ml = sml[w * 4 + j];
             const float f = ex2(ml.x - top);
             const float4* from = reinterpret_cast<const float4*>(
-                reinterpret_cast<const float*>(smem + dump_at[warp - tw + w]) + j * kDumpRow + 20 * c8);
+                reinterpret_cast<const float*>(smem + dump_at[warp - tw + w]) + j * kDumpRow + 20 * (c8 >> 1) +
+                8 * (c8 & 1));
             den = fmaf(f, ml.y, den);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const float4 v = from[c];
+              const float4 v = from[(c & 1) + 20 * (c >> 1)];  // dimensions 8 c8 .., then 64 on
               r[4 * c] = fmaf(f, v.x, r[4 * c]), r[4 * c + 1] = fmaf(f, v.y, r[4 * c + 1]);
               r[4 * c + 2] = fmaf(f, v.z, r[4 * c + 2]), r[4 * c + 3] = fmaf(f, v.w, r[4 * c + 3]);
             }

@@ -14,12 +14,16 @@
 // Every step is one IEEE fp32 operation and the butterfly strides run 1, 2, ...,
 // 64, so the stored bytes are a function of the input alone.
 //
-// Eight lanes a group, 16 consecutive values each: strides 1 to 8 in the lane,
-// 16 to 64 over lane distances 1, 2, 4.  The quotients v / s share one correctly
-// rounded reciprocal r and take three multiply-adds each, q0 = v r,
-// q0 + (v - q0 s) r: correctly rounded by Markstein's theorem (IBM Journal of
-// Research and Development 34, 1990), s having 11 significant bits and nothing
-// here nearing the ends of the exponent range.
+// Eight lanes a group, 16 values each: strides 1, 2, 4 and 64 in the lane, 8 to 32
+// over lane distances 1, 2, 4; a warp has four groups of one side (K or V,
+// which may differ in width) and strides over the tokens with its lanes' signs kept.
+// The quotients v / s share one correctly rounded reciprocal r and take three
+// multiply-adds each, q0 = v r, q0 + (v - q0 s) r: correctly rounded by Markstein's
+// theorem (IBM Journal of Research and Development 34, 1990), s having 11
+// significant bits and nothing here nearing the ends of the exponent range.
+// Bound by issue slots beside HBM: a rotated group costs 48 shuffles a warp of four,
+// so the rest is written in two-value operations (reading 30,001 rotated tokens of 8
+// heads took 574 instructions a warp and 84 us before, HBM's share being 26 us).
 #include "qlin_kv.cuh"
 
 namespace qlin {
@@ -28,7 +32,9 @@ namespace {
 __device__ unsigned int g_kv_error;
 
 constexpr int kThreads = 256;
-constexpr int kTasksPerCta = kThreads / 8;
+constexpr int kUnitsPerCta = kThreads / 16;  // groups of each side
+constexpr int kCtas = 4;  // an SM
+constexpr int kMaxGrid = 148 * kCtas;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
@@ -51,149 +57,245 @@ struct KvArgs {
   int32_t tokens;
 };
 
-// A task is one group of one token, head and side: order (token, head, side, group).
-struct Task {
-  bool live;
-  int side, g, bits, slot;
-  int64_t in;     // element offset of the group in the token rows (without the lane's 16 t)
-  uint8_t* row;   // the group's codes in the cache
-  uint8_t* par;   // the group's (scale, zero) pair of this side
+// A lane's walk over the groups (units) of its side: unit = (token, head, group), the group of 128
+// within the head fixed.
+struct Walk {
+  int side, g, bits, t;
+  int tok, r;         // token, and head * groups + group
+  int dtok, dr;       // a step
+  int unit, lg;       // units a token; log2 of the groups a head
+  int row_bytes;
+  int64_t row0, par0; // of the group in a block, at offset 0
+
+  __device__ __forceinline__ Walk(const KvArgs& a, int lane, int warp) {
+    lg = a.c.dim == kGroup ? 0 : 1;
+    unit = a.c.heads << lg;
+    const unsigned u = blockIdx.x * kUnitsPerCta + (warp >> 1) * 4 + (lane >> 3), step = gridDim.x * kUnitsPerCta;
+    t = lane & 7;
+    side = warp & 1;
+    bits = side ? a.c.v_bits : a.c.k_bits;
+    tok = (int)(u / (unsigned)unit);
+    r = (int)(u % (unsigned)unit);
+    dtok = (int)(step / (unsigned)unit);
+    dr = (int)(step % (unsigned)unit);
+    g = r & ((1 << lg) - 1);  // steps are even
+    row_bytes = side ? a.c.v_row : a.c.k_row;
+    row0 = (side ? a.c.v_offset : 0) + g * (kGroup / 8) * bits;
+    par0 = a.c.par_offset + 8 * g + 4 * side;
+  }
+  __device__ __forceinline__ void next() {
+    tok += dtok;
+    r += dr;
+    if (r >= unit) r -= unit, ++tok;
+  }
+  __device__ __forceinline__ int head() const { return r >> lg; }
+  // The group's codes in the cache, and its (scale, zero), for a slot inside the pool.
+  __device__ __forceinline__ void place(const KvArgs& a, int slot, uint8_t*& row, uint8_t*& par) const {
+    const int page = a.c.page_shift >= 0 ? slot >> a.c.page_shift : slot / a.c.page, off = slot - page * a.c.page;
+    uint8_t* b = a.c.pool + ((int64_t)page * a.c.heads + head()) * a.c.block_bytes;
+    row = b + row0 + (int64_t)off * row_bytes;
+    par = b + par0 + (int64_t)off * a.c.par;
+  }
 };
 
-__device__ __forceinline__ Task find_task(const KvArgs& a, int t, int64_t stride_k, int64_t stride_v) {
-  Task k;
-  const int lg = a.c.dim == kGroup ? 0 : 1, groups = 1 << lg, unit = a.c.heads * 2 * groups;  // tasks a token
-  // the block's first task by one division, the block's others by a short one
-  const unsigned base = blockIdx.x * (unsigned)kTasksPerCta, tok0 = base / (unsigned)unit;
-  const int x = (int)(base - tok0 * unit) + (int)(threadIdx.x >> 3), ahead = div_pos(x, unit);
-  int tok = (int)tok0 + ahead, r = x - ahead * unit;
-  k.live = tok < a.tokens;
-  if (!k.live) tok = a.tokens - 1, r = 0;
-  k.g = r & (groups - 1);
-  k.side = (r >> lg) & 1;
-  const int h = r >> (lg + 1);
-  k.bits = k.side ? a.c.v_bits : a.c.k_bits;
-  k.in = (int64_t)tok * (k.side ? stride_v : stride_k) + (int64_t)h * a.c.dim + (int64_t)k.g * kGroup;
-  k.slot = a.slots[tok];
-  if (k.slot >= a.c.pages * a.c.page) {
+// The slot of a token, or -1 where there is nothing to do.
+__device__ __forceinline__ int slot_of(const KvArgs& a, int tok, int t) {
+  int s = tok < a.tokens ? a.slots[tok] : -1;
+  if (s >= a.c.pages * a.c.page) {
     if (t == 0) atomicOr(&g_kv_error, kKvBadSlot);
-    k.slot = -1;
+    s = -1;
   }
-  const int s = k.slot < 0 ? 0 : k.slot;
-  const int page = a.c.page_shift >= 0 ? s >> a.c.page_shift : s / a.c.page, off = s - page * a.c.page;
-  uint8_t* b = const_cast<uint8_t*>(a.c.block(page, h));
-  k.row = b + (k.side ? a.c.v_offset() + (int64_t)off * a.c.v_row : (int64_t)off * a.c.k_row) + k.g * (kGroup / 8) * k.bits;
-  k.par = b + a.c.par_offset() + (int64_t)off * a.c.par + 8 * k.g + 4 * k.side;
-  return k;
+  return s;
 }
 
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
-  const int t = threadIdx.x & 7;
-  const Task k = find_task(a, t, a.k_stride, a.v_stride);
-  const __half* src = (k.side ? a.v_in : a.k_in) + k.in + 16 * t;
-  uint4 r0 = reinterpret_cast<const uint4*>(src)[0];
-  uint4 r1 = reinterpret_cast<const uint4*>(src)[1];
-  float v[16];
-  halves_to_float(r0, r1, v);
-  if (a.sign_bits) {
-    flip16(v, a.sign_bits[k.g * 4 + (t >> 1)] >> (16 * (t & 1)));
-    fwht128_oct(v, t);
-  }
-  const bool store = k.live && k.slot >= 0;
-  if (k.bits == 16) {  // both sides, or neither: uniform over the grid
-    if (a.sign_bits) float_to_halves(v, r0, r1);
-    if (store) {
-      reinterpret_cast<uint4*>(k.row)[2 * t] = r0;
-      reinterpret_cast<uint4*>(k.row)[2 * t + 1] = r1;
-    }
-    return;
-  }
-  float lo = 0.f, hi = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    lo = min_nan(lo, v[j]);
-    hi = max_nan(hi, v[j]);
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  lo = __fadd_rn(lo, 0.f);  // a zero bound is +0 whichever zero the reduction kept
-  const float qmax = (float)((1 << k.bits) - 1);
-  const float span = __fdiv_rn(__fsub_rn(hi, lo), qmax);
-  const bool finite = span < INFINITY;  // false for NaN too
-  __half s16 = __float2half_ru(fminf(span, 65504.f));
-  if (!(span > 0.f) || !finite) s16 = __float2half_rn(1.f);
-  const float s = __half2float(s16);
-  // a group that holds an infinity or NaN reads back as NaN throughout
-  const __half z16 = finite ? __float2half_rn(__fdiv_rn(-lo, s)) : __ushort_as_half(0x7fff);
-  const float z = __half2float(z16);
-  const float inv = __frcp_rn(s);
-  uint32_t q[16];  // the code in the low byte: adding 2^23 rounds to an integer, ties to even
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float q0 = __fmul_rn(v[j], inv), d = __fmaf_rn(__fmaf_rn(-q0, s, v[j]), inv, q0);
-    q[j] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fadd_rn(d, z), 0.f), qmax), 8388608.f));
-  }
-  if (!store) return;
-  if (k.bits == 8) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
-    reinterpret_cast<uint4*>(k.row)[t] = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t b[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) b[c] = q[8 * i + 2 * c] + (q[8 * i + 2 * c + 1] << 4);
-      w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    }
-    reinterpret_cast<uint2*>(k.row)[t] = make_uint2(w[0], w[1]);
-  }
-  if (t == 0) *reinterpret_cast<__half2*>(k.par) = __halves2half2(s16, z16);
-}
+// The loops below keep the next unit's data and the slot of the one after it in flight.
 
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
-  const int t = threadIdx.x & 7;
-  const int64_t row = (int64_t)a.c.heads * a.c.dim;
-  const Task k = find_task(a, t, row, row);
-  uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
-  float v[16];
-  if (k.bits == 16) {
-    r0 = reinterpret_cast<const uint4*>(k.row)[2 * t];
-    r1 = reinterpret_cast<const uint4*>(k.row)[2 * t + 1];
-    halves_to_float(r0, r1, v);
-  } else {
-    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(k.par));
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (k.bits == 8) {
-      const uint4 c = reinterpret_cast<const uint4*>(k.row)[t];
-      w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        v[j] = __fmul_rn(p.x, __fsub_rn((float)((w[j >> 2] >> (8 * (j & 3))) & 255u), p.y));
+__global__ void __launch_bounds__(kThreads, kCtas) kv_write_kernel(const __grid_constant__ KvArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Walk w(a, lane, warp);
+  const int64_t stride = w.side ? a.v_stride : a.k_stride;
+  const uint4* src = reinterpret_cast<const uint4*>((w.side ? a.v_in : a.k_in) + w.g * kGroup) + w.t;
+  uint32_t flip[8];
+  if (a.sign_bits) sign_masks(a.sign_bits + 4 * w.g, w.t, flip);
+  uint4 n0, n1;
+  auto load = [&]() {
+    const int64_t at = (int64_t)min(w.tok, a.tokens - 1) * stride + (int64_t)w.head() * a.c.dim;
+    n0 = src[at >> 3], n1 = src[(at >> 3) + 8];
+  };
+  int next_slot = slot_of(a, w.tok, w.t);
+  load();
+  while (__any_sync(0xffffffffu, w.tok < a.tokens)) {
+    const int slot = next_slot;
+    uint4 r0 = n0, r1 = n1;
+    uint8_t *row, *par;
+    w.place(a, max(slot, 0), row, par);
+    w.next();
+    next_slot = slot_of(a, w.tok, w.t);
+    load();
+    f32x2 v[8];
+    if (a.sign_bits) {
+      flip16(r0, r1, flip);
+      halves_to_float(r0, r1, v);
+      fwht128_oct(v, w.t);
+      if (w.bits == 16) float_to_halves(v, r0, r1);
     } else {
-      const uint2 c = reinterpret_cast<const uint2*>(k.row)[t];
-      w[0] = c.x, w[1] = c.y;
+      halves_to_float(r0, r1, v);
+    }
+    if (w.bits == 16) {
+      if (slot >= 0) {
+        reinterpret_cast<uint4*>(row)[w.t] = r0;
+        reinterpret_cast<uint4*>(row)[w.t + 8] = r1;
+      }
+      continue;
+    }
+    float lo = 0.f, hi = 0.f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        v[j] = __fmul_rn(p.x, __fsub_rn((float)((w[j >> 3] >> (4 * (j & 7))) & 15u), p.y));
+    for (int j = 0; j < 8; ++j) {
+      float x, y;
+      split2(v[j], x, y);
+      lo = min_nan(lo, min_nan(x, y));
+      hi = max_nan(hi, max_nan(x, y));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    lo = __fadd_rn(lo, 0.f);  // a zero bound is +0 whichever zero the reduction kept
+    const float qmax = (float)((1 << w.bits) - 1);
+    const float span = __fdiv_rn(__fsub_rn(hi, lo), qmax);
+    const bool finite = span < INFINITY;  // false for NaN too
+    __half s16 = __float2half_ru(fminf(span, 65504.f));
+    if (!(span > 0.f) || !finite) s16 = __float2half_rn(1.f);
+    const float s = __half2float(s16);
+    // a group that holds an infinity or NaN reads back as NaN throughout
+    const __half z16 = finite ? __float2half_rn(__fdiv_rn(-lo, s)) : __ushort_as_half(0x7fff);
+    const float z = __half2float(z16), inv = __frcp_rn(s);
+    // v / s + z lies within 1/16 of [0, qmax] unless the scale was cut or the group is not finite
+    const bool clamp = !(span <= 65504.f);
+    const f32x2 s2 = pair2(-s, -s), inv2 = pair2(inv, inv), z2 = pair2(z, z), round2 = pair2(8388608.f, 8388608.f);
+    uint32_t q[16];  // the code in the low byte: adding 2^23 rounds to an integer, ties to even
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const f32x2 q0 = mul2(v[j], inv2);
+      f32x2 y = add2(fma2(fma2(q0, s2, v[j]), inv2, q0), z2);
+      float y0, y1;
+      if (clamp) {
+        split2(y, y0, y1);
+        y = pair2(fminf(fmaxf(y0, 0.f), qmax), fminf(fmaxf(y1, 0.f), qmax));
+      }
+      split2(add2(y, round2), y0, y1);
+      q[2 * j] = __float_as_uint(y0);
+      q[2 * j + 1] = __float_as_uint(y1);
+    }
+    if (slot < 0) continue;
+    if (w.bits == 8) {
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040),
+                           0x5410);
+      reinterpret_cast<uint2*>(row)[w.t] = make_uint2(c[0], c[1]);
+      reinterpret_cast<uint2*>(row)[w.t + 8] = make_uint2(c[2], c[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = q[8 * i + 2 * k] + (q[8 * i + 2 * k + 1] << 4);
+        reinterpret_cast<uint32_t*>(row)[w.t + 8 * i] =
+            __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      }
+    }
+    if (w.t == 0) *reinterpret_cast<__half2*>(par) = __halves2half2(s16, z16);
+  }
+}
+
+// s (q - z) of two codes a 2^23 + q U, U = 16^k the weight of the bits they sit on: taking 2^23 off
+// is exact, the multiply-add with 1 / U rounds q - z once, the product with s once.
+__device__ __forceinline__ f32x2 dequant2(uint32_t a, uint32_t b, f32x2 inv_unit, f32x2 z, f32x2 s) {
+  const f32x2 x = add2(pair2(__uint_as_float(a), __uint_as_float(b)), pair2(-8388608.f, -8388608.f));
+  return mul2(s, fma2(x, inv_unit, z));
+}
+
+__global__ void __launch_bounds__(kThreads, kCtas) kv_read_kernel(const __grid_constant__ KvArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Walk w(a, lane, warp);
+  const int64_t stride = (int64_t)a.c.heads * a.c.dim;
+  uint4* dst = reinterpret_cast<uint4*>((w.side ? a.v_out : a.k_out) + w.g * kGroup) + w.t;
+  uint32_t flip[8];
+  if (a.sign_bits) sign_masks(a.sign_bits + 4 * w.g, w.t, flip);
+  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+  uint32_t next_par = 0;
+  auto load = [&](int slot) {
+    uint8_t *row, *par;
+    w.place(a, max(slot, 0), row, par);
+    if (w.bits == 16) {
+      n0 = reinterpret_cast<const uint4*>(row)[w.t];
+      n1 = reinterpret_cast<const uint4*>(row)[w.t + 8];
+    } else {
+      next_par = *reinterpret_cast<const uint32_t*>(par);
+      if (w.bits == 8) {
+        const uint2 c = reinterpret_cast<const uint2*>(row)[w.t], d = reinterpret_cast<const uint2*>(row)[w.t + 8];
+        n0 = make_uint4(c.x, c.y, d.x, d.y);
+      } else {
+        n0.x = reinterpret_cast<const uint32_t*>(row)[w.t];
+        n0.y = reinterpret_cast<const uint32_t*>(row)[w.t + 8];
+      }
+    }
+  };
+  int next_slot = slot_of(a, w.tok, w.t);
+  load(next_slot);
+  int tok = w.tok, head = w.head();  // of the unit in n0, n1
+  w.next();
+  int after = slot_of(a, w.tok, w.t);
+  while (__any_sync(0xffffffffu, tok < a.tokens)) {
+    const int slot = next_slot;
+    uint4 r0 = n0, r1 = n1;
+    const uint32_t pp = next_par;
+    uint4* out = dst + (((int64_t)tok * stride + (int64_t)head * a.c.dim) >> 3);
+    const bool live = tok < a.tokens;
+    load(after);
+    next_slot = after;
+    tok = w.tok, head = w.head();
+    w.next();
+    after = slot_of(a, w.tok, w.t);
+    f32x2 v[8];
+    if (w.bits == 16) {
+      if (a.sign_bits) halves_to_float(r0, r1, v);
+    } else {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pp));
+      const f32x2 s = pair2(p.x, p.x), z = pair2(-p.y, -p.y);
+      const uint32_t x[4] = {r0.x, r0.y, r0.z, r0.w};
+      if (w.bits == 8) {
+        const f32x2 one = pair2(1.f, 1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            v[2 * i + k] = dequant2(__byte_perm(x[i], 0x4B000000u, 0x7440 + 2 * k),
+                                    __byte_perm(x[i], 0x4B000000u, 0x7441 + 2 * k), one, z, s);
+      } else {
+        const f32x2 u0 = pair2(1.f, 0.0625f), u2 = pair2(0x1p-8f, 0x1p-12f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t y = x[i] >> (16 * k);
+            v[4 * i + 2 * k] = dequant2((y & 0xFu) | 0x4B000000u, (y & 0xF0u) | 0x4B000000u, u0, z, s);
+            v[4 * i + 2 * k + 1] = dequant2((y & 0xF00u) | 0x4B000000u, (y & 0xF000u) | 0x4B000000u, u2, z, s);
+          }
+      }
+    }
+    if (a.sign_bits) fwht128_oct(v, w.t);
+    if (a.sign_bits || w.bits != 16) float_to_halves(v, r0, r1);
+    if (a.sign_bits) flip16(r0, r1, flip);
+    if (slot < 0) r0 = r1 = make_uint4(0u, 0u, 0u, 0u);
+    if (live) {
+      out[0] = r0;
+      out[8] = r1;
     }
   }
-  if (a.sign_bits) {
-    fwht128_oct(v, t);
-    flip16(v, a.sign_bits[k.g * 4 + (t >> 1)] >> (16 * (t & 1)));
-  }
-  if (a.sign_bits || k.bits != 16) float_to_halves(v, r0, r1);
-  if (k.slot < 0) r0 = r1 = make_uint4(0u, 0u, 0u, 0u);
-  if (!k.live) return;
-  uint4* dst = reinterpret_cast<uint4*>((k.side ? a.v_out : a.k_out) + k.in + 16 * t);
-  dst[0] = r0;
-  dst[1] = r1;
 }
 
 }  // namespace
@@ -205,11 +307,12 @@ unsigned take_kv_error() {
   return v;
 }
 
-// Tasks are counted in 31 bits.
+// Units and a step beyond them are counted in 31 bits.
 static qlin_status kv_grid(const KvArgs& a, unsigned* grid) {
-  const int64_t tasks = (int64_t)a.tokens * a.c.heads * 2 * (a.c.dim / kGroup);
-  if (tasks > 0x7fffffffLL - kTasksPerCta) return QLIN_ERR_SHAPE;
-  *grid = (unsigned)((tasks + kTasksPerCta - 1) / kTasksPerCta);
+  const int64_t units = (int64_t)a.tokens * a.c.heads * (a.c.dim / kGroup);
+  if (units > 0x7fffffffLL - 2 * kMaxGrid * kUnitsPerCta) return QLIN_ERR_SHAPE;
+  const int64_t need = (units + kUnitsPerCta - 1) / kUnitsPerCta;
+  *grid = (unsigned)(need < kMaxGrid ? need : kMaxGrid);
   return QLIN_OK;
 }
 

@@ -21,7 +21,8 @@ constexpr int kItemExtra = 32; // most that attention adds to an item's tiles wh
 
 struct KvView {
   uint8_t* pool;
-  int64_t block_bytes;  // one (page, head) block
+  int64_t block_bytes;        // one (page, head) block
+  int64_t v_offset, par_offset;  // of its V rows and parameters
   int32_t pages, page, heads, dim;
   int32_t k_bits, v_bits;
   int32_t k_row, v_row;  // bytes of a row
@@ -31,8 +32,6 @@ struct KvView {
   __host__ __device__ const uint8_t* block(int p, int h) const {
     return pool + ((int64_t)p * heads + h) * block_bytes;
   }
-  __host__ __device__ int64_t v_offset() const { return (int64_t)page * k_row; }
-  __host__ __device__ int64_t par_offset() const { return (int64_t)page * (k_row + v_row); }
 };
 
 __host__ inline KvView make_kv_view(const qlin_kv_desc* d, const void* cache) {
@@ -48,7 +47,9 @@ __host__ inline KvView make_kv_view(const qlin_kv_desc* d, const void* cache) {
   v.k_row = d->head_dim * d->k_bits / 8;
   v.v_row = d->head_dim * d->v_bits / 8;
   v.par = d->k_bits == 16 ? 0 : 8 * (d->head_dim / kGroup);
-  v.block_bytes = (int64_t)d->page_size * (v.k_row + v.v_row + v.par);
+  v.v_offset = (int64_t)d->page_size * v.k_row;
+  v.par_offset = v.v_offset + (int64_t)d->page_size * v.v_row;
+  v.block_bytes = v.par_offset + (int64_t)d->page_size * v.par;
   return v;
 }
 
@@ -77,54 +78,106 @@ __device__ __forceinline__ int div_pos(int n, int d) {
   return q + (rest >= d);
 }
 
-// A group of 128 values on eight lanes, lane t = lane % 8 with values 16 t .. 16 t + 15.
+// A group of 128 values on eight lanes: lane t = lane % 8 has values 8 t .. 8 t + 7 (v[0..7]) and
+// 64 + 8 t .. 64 + 8 t + 7 (v[8..15]), so that 16-byte pieces of halves are contiguous over the lanes.
 
-// Butterflies of strides 1..64 over the 16 values of each of a group's eight lanes.
-__device__ __forceinline__ void fwht128_oct(float (&v)[16], int t) {
+// Two fp32 values in one register pair; each operation rounds both to nearest, like two single ones.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// Butterflies of strides 1..64 (1, 2, 4 in the lane, 8, 16, 32 across lanes, 64 in the lane), then
+// the scaling.  A difference a - b is the multiply-add b (-1) + a, and across lanes both halves are
+// v (+-1) + p: one rounding each, as the definition has it.
+__device__ __forceinline__ void fwht128_oct(f32x2 (&p)[8], int t) {
+  const f32x2 minus = pair2(-1.f, -1.f);
 #pragma unroll
-  for (int h = 1; h < 16; h <<= 1)
+  for (int j = 0; j < 8; ++j) {
+    float a, b;
+    split2(p[j], a, b);
+    p[j] = pair2(__fadd_rn(a, b), __fsub_rn(a, b));
+  }
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+  for (int h = 1; h < 4; h <<= 1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
       if (!(j & h)) {
-        const float a = v[j], b = v[j + h];
-        v[j] = __fadd_rn(a, b);
-        v[j + h] = __fsub_rn(a, b);
+        const f32x2 a = p[j], b = p[j + h];
+        p[j] = add2(a, b);
+        p[j + h] = fma2(b, minus, a);
       }
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
-    const bool upper = (t & o) != 0;
+    const float sign = (t & o) ? -1.f : 1.f;
+    const f32x2 s = pair2(sign, sign);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float p = __shfl_xor_sync(0xffffffffu, v[j], o);
-      v[j] = upper ? __fsub_rn(p, v[j]) : __fadd_rn(v[j], p);
+    for (int j = 0; j < 8; ++j) {
+      float lo, hi;
+      split2(p[j], lo, hi);
+      p[j] = fma2(p[j], s, pair2(__shfl_xor_sync(0xffffffffu, lo, o), __shfl_xor_sync(0xffffffffu, hi, o)));
     }
   }
+  const f32x2 scale = pair2(kInvSqrt128, kInvSqrt128);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], kInvSqrt128);
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 a = p[j], b = p[j + 4];
+    p[j] = mul2(add2(a, b), scale);
+    p[j + 4] = mul2(fma2(b, minus, a), scale);
+  }
 }
 
-// Changes the signs of the lane's values of group g.
-__device__ __forceinline__ void flip16(float (&v)[16], uint32_t sw) {
+// Sign masks of the lane's 16 values, as eight pairs of halves; `words` are the group's four.
+__device__ __forceinline__ void sign_masks(const uint32_t* words, int t, uint32_t (&m)[8]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    v[j] = __uint_as_float(__float_as_uint(v[j]) ^ (((sw >> j) & 1u) << 31));
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t sw = words[2 * k + (t >> 2)] >> (8 * (t & 3));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[4 * k + i] = ((sw >> (2 * i)) & 1u) << 15 | ((sw >> (2 * i + 1)) & 1u) << 31;
+  }
 }
 
-__device__ __forceinline__ void halves_to_float(const uint4& r0, const uint4& r1, float (&v)[16]) {
+__device__ __forceinline__ void flip16(uint4& r0, uint4& r1, const uint32_t (&m)[8]) {
+  r0.x ^= m[0], r0.y ^= m[1], r0.z ^= m[2], r0.w ^= m[3];
+  r1.x ^= m[4], r1.y ^= m[5], r1.z ^= m[6], r1.w ^= m[7];
+}
+
+__device__ __forceinline__ void halves_to_float(const uint4& r0, const uint4& r1, f32x2 (&v)[8]) {
   const uint32_t raw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    v[i] = pair2(f.x, f.y);
   }
 }
 
-__device__ __forceinline__ void float_to_halves(const float (&v)[16], uint4& r0, uint4& r1) {
+__device__ __forceinline__ void float_to_halves(const f32x2 (&v)[8], uint4& r0, uint4& r1) {
   uint32_t raw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    float a, b;
+    split2(v[i], a, b);
+    const __half2 h = __floats2half2_rn(a, b);
     raw[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   r0 = make_uint4(raw[0], raw[1], raw[2], raw[3]);
