@@ -98,14 +98,15 @@ struct Walk {
   }
 };
 
-// The slot of a token, or -1 where there is nothing to do.
-__device__ __forceinline__ int slot_of(const KvArgs& a, int tok, int t) {
-  int s = tok < a.tokens ? a.slots[tok] : -1;
-  if (s >= a.c.pages * a.c.page) {
-    if (t == 0) atomicOr(&g_kv_error, kKvBadSlot);
-    s = -1;
-  }
-  return s;
+// The slot of a token as given, -1 past the last; it is looked at (checked_slot) one step later, so
+// that no step waits for this load.
+__device__ __forceinline__ int slot_of(const KvArgs& a, int tok) { return tok < a.tokens ? a.slots[tok] : -1; }
+
+// A slot inside the pool, or -1 where there is nothing to do.
+__device__ __forceinline__ int checked_slot(const KvArgs& a, int s, int t) {
+  if (s < a.c.pages * a.c.page) return max(s, -1);
+  if (t == 0) atomicOr(&g_kv_error, kKvBadSlot);
+  return -1;
 }
 
 // The loops below keep the next unit's data and the slot of the one after it in flight.
@@ -122,15 +123,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_write_kernel(const __grid_
     const int64_t at = (int64_t)min(w.tok, a.tokens - 1) * stride + (int64_t)w.head() * a.c.dim;
     n0 = src[at >> 3], n1 = src[(at >> 3) + 8];
   };
-  int next_slot = slot_of(a, w.tok, w.t);
+  int next_slot = slot_of(a, w.tok);
   load();
   while (__any_sync(0xffffffffu, w.tok < a.tokens)) {
-    const int slot = next_slot;
+    const int slot = checked_slot(a, next_slot, w.t);
     uint4 r0 = n0, r1 = n1;
     uint8_t *row, *par;
     w.place(a, max(slot, 0), row, par);
     w.next();
-    next_slot = slot_of(a, w.tok, w.t);
+    next_slot = slot_of(a, w.tok);
     load();
     f32x2 v[8];
     if (a.sign_bits) {
@@ -244,22 +245,22 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_read_kernel(const __grid_c
       }
     }
   };
-  int next_slot = slot_of(a, w.tok, w.t);
+  int next_slot = checked_slot(a, slot_of(a, w.tok), w.t);
   load(next_slot);
   int tok = w.tok, head = w.head();  // of the unit in n0, n1
   w.next();
-  int after = slot_of(a, w.tok, w.t);
+  int after = slot_of(a, w.tok);
   while (__any_sync(0xffffffffu, tok < a.tokens)) {
     const int slot = next_slot;
     uint4 r0 = n0, r1 = n1;
     const uint32_t pp = next_par;
     uint4* out = dst + (((int64_t)tok * stride + (int64_t)head * a.c.dim) >> 3);
     const bool live = tok < a.tokens;
-    load(after);
-    next_slot = after;
+    next_slot = checked_slot(a, after, w.t);
+    load(next_slot);
     tok = w.tok, head = w.head();
     w.next();
-    after = slot_of(a, w.tok, w.t);
+    after = slot_of(a, w.tok);
     f32x2 v[8];
     if (w.bits == 16) {
       if (a.sign_bits) halves_to_float(r0, r1, v);

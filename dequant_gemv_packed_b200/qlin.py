@@ -371,10 +371,22 @@ def qlin_linear_host(desc: Desc, packed, scales, zeros, sign_bits, x_host, y_hos
 
 
 # ------------------------------------------------- the decode step between the layers
+#
+# These calls run once or more a layer and token, so a call with a stream of its own or on another
+# device goes through _elsewhere, and the others check each tensor in one expression.
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _elsewhere(t, stream) -> bool:
+    """Whether a call on `t` needs another device or stream made current first."""
+    return (stream is not None or not isinstance(t, torch.Tensor) or not t.is_cuda
+            or t.get_device() != _current_device())
+
 
 def _on(t: torch.Tensor, stream):
-    """Context of a call on `t`'s device and `stream`: makes the device current, and
-    allocates outputs and workspaces on the stream that uses them."""
+    """Makes `t`'s device and `stream` current, so that outputs and workspaces are allocated on the
+    stream that uses them."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("the call takes CUDA tensors: its buffers must each be a CUDA tensor")
     if stream is None:
@@ -384,39 +396,45 @@ def _on(t: torch.Tensor, stream):
     return torch.cuda.stream(stream)
 
 
-def _same_device(like: torch.Tensor, **tensors) -> None:
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+def _ptr(t: torch.Tensor, dtype, name: str, dev: int) -> int:
+    """Address of a contiguous tensor of `dtype` on CUDA device `dev`."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
-def _heads(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
-    """Element stride between the token rows of t [T, heads, dim], whose heads are contiguous."""
+def _rows(t: torch.Tensor, heads: int, dim: int, name: str, dev: int) -> int:
+    """Element stride between the token rows of t [T, heads, dim] fp16, whose heads are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {list(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {list(shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"the heads of {name} must be contiguous")
-    return heads * dim if t.shape[0] == 1 else t.stride(0)
+    return heads * dim if shape[0] == 1 else st[0]
 
 
-def _cache(desc: KVDesc, cache: torch.Tensor) -> int:
+def _cache(desc: KVDesc, cache: torch.Tensor, dev: int) -> int:
     if desc._bytes is None:
         desc._bytes = qlin_kv_cache_bytes(desc)
-    p = _dev(cache, torch.uint8, "cache")
+    p = _ptr(cache, torch.uint8, "cache", dev)
     if cache.numel() < desc._bytes:
         raise ValueError("cache buffer too small")
     return p
 
 
-def _signs(desc: KVDesc, sign_bits: Optional[torch.Tensor]):
+def _signs(desc: KVDesc, sign_bits: Optional[torch.Tensor], dev: int):
     if sign_bits is None:
         return None
-    p = _dev(sign_bits, torch.int32, "sign_bits")
-    if sign_bits.numel() != desc.head_dim // 32:
+    p = _ptr(sign_bits, torch.int32, "sign_bits", dev)
+    if sign_bits.numel() * 32 != desc.head_dim:
         raise ValueError("sign_bits must hold head_dim bits")
     return p
 
@@ -429,31 +447,43 @@ def qlin_kv_write(desc: KVDesc, cache: torch.Tensor, k: torch.Tensor, v: torch.T
                   sign_bits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Quantise the keys and values [T, kv_heads, head_dim] (rows may be columns of a wider
     matrix) into the cache at `slots` [T] int32, negative ones skipped; returns the cache."""
-    with _on(cache, stream):
-        _same_device(cache, k=k, v=v, slots=slots, sign_bits=sign_bits)
-        ks, vs = _heads(k, desc.kv_heads, desc.head_dim, "k"), _heads(v, desc.kv_heads, desc.head_dim, "v")
-        sp = _dev(slots, torch.int32, "slots")
-        if v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
-            raise ValueError("k, v and slots must have one row per token")
-        _check(lib().qlin_kv_write(desc.ref(), _cache(desc, cache), k.data_ptr(), v.data_ptr(), ks, vs, sp, k.shape[0],
-                                   _signs(desc, sign_bits), _stream(stream, cache)), "qlin_kv_write")
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return qlin_kv_write(desc, cache, k, v, slots, sign_bits)
+    dev = cache.get_device()
+    ks, vs = _rows(k, desc.kv_heads, desc.head_dim, "k", dev), _rows(v, desc.kv_heads, desc.head_dim, "v", dev)
+    sp, T = _ptr(slots, torch.int32, "slots", dev), k.shape[0]
+    if v.shape[0] != T or slots.numel() != T:
+        raise ValueError("k, v and slots must have one row per token")
+    st = (_lib or lib()).qlin_kv_write(desc._byref, _cache(desc, cache, dev), k.data_ptr(), v.data_ptr(), ks, vs, sp, T,
+                                       _signs(desc, sign_bits, dev), _stream(None, cache))
+    if st:
+        raise QlinError(st, "qlin_kv_write")
     return cache
 
 
 def qlin_kv_read(desc: KVDesc, cache: torch.Tensor, slots: torch.Tensor, sign_bits: Optional[torch.Tensor] = None,
                  k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
     """Keys and values [T, kv_heads, head_dim] fp16 at `slots` [T] int32 (zeros for negative ones)."""
-    with _on(cache, stream):
-        _same_device(cache, slots=slots, sign_bits=sign_bits, k=k, v=v)
-        sp = _dev(slots, torch.int32, "slots")
-        shape = (slots.numel(), desc.kv_heads, desc.head_dim)
-        k = _alloc(shape, torch.float16, cache) if k is None else k
-        v = _alloc(shape, torch.float16, cache) if v is None else v
-        if tuple(k.shape) != shape or tuple(v.shape) != shape:
-            raise ValueError(f"k and v must be {list(shape)}")
-        _check(lib().qlin_kv_read(desc.ref(), _cache(desc, cache), sp, shape[0], _signs(desc, sign_bits),
-                                  _dev(k, torch.float16, "k"), _dev(v, torch.float16, "v"), _stream(stream, cache)),
-               "qlin_kv_read")
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return qlin_kv_read(desc, cache, slots, sign_bits, k, v)
+    dev = cache.get_device()
+    sp = _ptr(slots, torch.int32, "slots", dev)
+    shape = (slots.numel(), desc.kv_heads, desc.head_dim)
+    if k is None:
+        k = cache.new_empty(shape, dtype=torch.float16)
+    elif tuple(k.shape) != shape:
+        raise ValueError(f"k must be {list(shape)}")
+    if v is None:
+        v = torch.empty_like(k)
+    elif tuple(v.shape) != shape:
+        raise ValueError(f"v must be {list(shape)}")
+    st = (_lib or lib()).qlin_kv_read(desc._byref, _cache(desc, cache, dev), sp, shape[0], _signs(desc, sign_bits, dev),
+                                      _ptr(k, torch.float16, "k", dev), _ptr(v, torch.float16, "v", dev),
+                                      _stream(None, cache))
+    if st:
+        raise QlinError(st, "qlin_kv_read")
     return k, v
 
 
@@ -468,31 +498,35 @@ def qlin_attn_decode(desc: KVDesc, cache: torch.Tensor, q: torch.Tensor, block_t
     """Attention of one new token per sequence, q [B, q_heads, head_dim], over the cached tokens
     t < seq_lens[b] (int32 [B]) in the pages block_table [B, max_pages] (int32); scale defaults
     to 1 / sqrt(head_dim).  Returns [B, q_heads, head_dim]."""
-    with _on(cache, stream):
-        _same_device(cache, q=q, block_table=block_table, seq_lens=seq_lens, sign_bits=sign_bits, out=out,
-                     workspace=workspace)
-        if q.dim() != 3:
-            raise ValueError("q must be [B, q_heads, head_dim]")
-        B, Hq, D = q.shape
-        qs = _heads(q, Hq, desc.head_dim, "q")
-        tp, lp = _dev(block_table, torch.int32, "block_table"), _dev(seq_lens, torch.int32, "seq_lens")
-        if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
-            raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-        if out is None:
-            out = _alloc((B, Hq, D), torch.float16, q)
-        elif tuple(out.shape) != (B, Hq, D):
-            raise ValueError("out must be [B, q_heads, head_dim]")
-        mp = block_table.shape[1]
-        ws = desc._ws.get((Hq, B, mp))
-        if ws is None:
-            ws = desc._ws[(Hq, B, mp)] = qlin_attn_workspace_bytes(desc, Hq, B, mp)
-        if workspace is None and ws:
-            workspace = _alloc((ws,), torch.uint8, q)
-        wp, wl = (None, 0) if workspace is None else (_dev(workspace, torch.uint8, "workspace"), workspace.numel())
-        _check(lib().qlin_attn_decode(desc.ref(), _cache(desc, cache), q.data_ptr(), qs, Hq, tp, mp, lp, B,
-                                      _signs(desc, sign_bits), desc.head_dim ** -0.5 if scale is None else scale,
-                                      _dev(out, torch.float16, "out"), wp, wl, _stream(stream, cache)),
-               "qlin_attn_decode")
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return qlin_attn_decode(desc, cache, q, block_table, seq_lens, scale, sign_bits, out, workspace)
+    dev = cache.get_device()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [B, q_heads, head_dim]")
+    shape = q.shape
+    B, Hq, _ = shape
+    qs = _rows(q, Hq, desc.head_dim, "q", dev)
+    tp, lp = _ptr(block_table, torch.int32, "block_table", dev), _ptr(seq_lens, torch.int32, "seq_lens", dev)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.shape != shape:
+        raise ValueError("out must be [B, q_heads, head_dim]")
+    mp = block_table.shape[1]
+    ws = desc._ws.get((Hq, B, mp))
+    if ws is None:
+        ws = desc._ws[(Hq, B, mp)] = qlin_attn_workspace_bytes(desc, Hq, B, mp)
+    if workspace is None and ws:
+        workspace = cache.new_empty(ws)
+    wp, wl = (None, 0) if workspace is None else (_ptr(workspace, torch.uint8, "workspace", dev), workspace.numel())
+    st = (_lib or lib()).qlin_attn_decode(desc._byref, _cache(desc, cache, dev), q.data_ptr(), qs, Hq, tp, mp, lp, B,
+                                          _signs(desc, sign_bits, dev),
+                                          desc.head_dim ** -0.5 if scale is None else scale,
+                                          _ptr(out, torch.float16, "out", dev), wp, wl, _stream(None, cache))
+    if st:
+        raise QlinError(st, "qlin_attn_decode")
     return out
 
 
@@ -500,20 +534,31 @@ def qlin_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
                  y: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None, stream=None):
     """Root-mean-square norm of the rows of x [M, K], after the addition of `residual` if given:
     y, or (y, the new residual).  residual_out may be `residual` itself."""
-    with _on(x, stream):
-        _same_device(x, weight=weight, residual=residual, y=y, residual_out=residual_out)
-        M, K = x.shape
-        if weight.numel() != K or any(t is not None and tuple(t.shape) != (M, K) for t in (residual, y, residual_out)):
-            raise ValueError("shapes: x, residual, y, residual_out [M, K], weight [K]")
-        if residual is None and residual_out is not None:
-            raise ValueError("residual_out without a residual")
-        y = torch.empty_like(x) if y is None else y
-        rp = op = None
-        if residual is not None:
-            residual_out = torch.empty_like(x) if residual_out is None else residual_out
-            rp, op = _dev(residual, torch.float16, "residual"), _dev(residual_out, torch.float16, "residual_out")
-        _check(lib().qlin_rmsnorm(_dev(x, torch.float16, "x"), rp, _dev(weight, torch.float16, "weight"), eps,
-                                  _dev(y, torch.float16, "y"), op, M, K, _stream(stream, x)), "qlin_rmsnorm")
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return qlin_rmsnorm(x, weight, eps, residual, y, residual_out)
+    dev, shape = x.get_device(), x.shape
+    M, K = shape
+    xp, wp = _ptr(x, torch.float16, "x", dev), _ptr(weight, torch.float16, "weight", dev)
+    if weight.numel() != K:
+        raise ValueError("weight must be [K]")
+    if y is None:
+        y = torch.empty_like(x)
+    elif y.shape != shape:
+        raise ValueError("y must be [M, K]")
+    rp = op = None
+    if residual is not None:
+        rp = _ptr(residual, torch.float16, "residual", dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        if residual.shape != shape or residual_out.shape != shape:
+            raise ValueError("residual and residual_out must be [M, K]")
+        op = _ptr(residual_out, torch.float16, "residual_out", dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    st = (_lib or lib()).qlin_rmsnorm(xp, rp, wp, eps, _ptr(y, torch.float16, "y", dev), op, M, K, _stream(None, x))
+    if st:
+        raise QlinError(st, "qlin_rmsnorm")
     return y if residual is None else (y, residual_out)
 
 
