@@ -31,7 +31,7 @@
 // the next product's operand; a query's statistics live in the lanes that scale its
 // sums.  S^T = K Q^T has the tile's 16 tokens as rows, O^T = V^T P^T 16 dimensions.
 // More than four queries take a second set of columns on the same decoded codes
-// (kNt = 2), more than eight a second pass over the cache.
+// (NT = 2), more than eight (four of 256 dimensions) another pass over the cache.
 //
 // Split.  A tile is 16 tokens of one (sequence, kv head, block of queries), an item
 // all tiles of one.  Items in order, each its tiles plus a constant for what an item
@@ -69,7 +69,10 @@ constexpr int kSms = 148;
 constexpr float kNone = -1e30f;   // running maximum of a warp that has seen no token
 constexpr int kWholeTiles = 32;   // items up to here are not cut
 constexpr int kMinShare = 16;     // tiles a team when they are
-constexpr int kExtraWarp = 8, kExtraTeam = 24;  // an item's cost beside its tiles, in tiles of a warp alone, of a team
+// An item's cost beside its tiles, in tiles, for a team of T warps: fitted to 1,592 items of up to 32
+// tiles (29.3, 24.5, 24.3 and 33.4 us with one, two, four and eight warps) and to 16 long sequences
+// among short ones (28.3 us at 16 for eight warps, 24.7 at 24, 24.7 at 32).
+__device__ __forceinline__ int item_extra(int lt) { return 4 + (4 << lt); }
 // A warp's sums in shared memory: 16 values every 20 floats, which spreads both the lanes that
 // write (16 dimensions of a query each) and those that read over the banks.
 constexpr int kDumpRow = 8 * 20 + 8;  // of a query
@@ -88,8 +91,9 @@ struct Cfg {
   static constexpr int kAlign = KB == 16 ? 256 : 128;
   static constexpr int kStage = ((kTileBytes > kDump ? kTileBytes : kDump) + 16 + kAlign - 1) / kAlign * kAlign;
   // 32 accumulators a warp (one group, four queries) leave room for 16 warps an SM at 128
-  // registers; 64 for 12 at 168, 128 for 8 at 255.  16-bit rows fill the rings: 8 warps.
+  // registers; 64 (two groups, or eight queries) for 12 at 168.  16-bit rows fill the rings: 8 warps.
   static constexpr int kSets = NG * NT;
+  static_assert(kSets <= 2, "registers");
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
   static constexpr int kSmemQ = kWarps * NT * NG * 1024;        // operand of the queries, a team
   static constexpr int kSmemX = kWarps * kRowQ * NG * 8;        // (scale, sum) of each, a team
@@ -163,10 +167,17 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
   Plan p;
   p.cut = a.may_cut && top > kWholeTiles;
   p.lt = 31 - __clz(warps);
-  if (!p.cut)
-    while (p.lt > 0 && live > grid * (warps >> p.lt)) --p.lt;
-  p.extra = p.lt ? kExtraTeam : kExtraWarp;
-  static_assert(kExtraWarp <= kItemExtra && kExtraTeam <= kItemExtra, "positions are counted in an int");
+  if (!p.cut) {
+    // the longest item on one team, or all items on all warps, in tiles of a warp: the least
+    int best = 0x7fffffff;
+    for (int lt = p.lt; lt >= 0; --lt) {
+      const int e = item_extra(lt), all = (int)(((int64_t)n * a.items + (int64_t)live * e) / (grid * warps));
+      const int cost = max((top + e) >> lt, all);
+      if (cost < best) best = cost, p.lt = lt;
+    }
+  }
+  p.extra = item_extra(p.lt);
+  static_assert(4 + 4 * warps <= kItemExtra, "positions are counted in an int");
   p.total = n * a.items + live * p.extra;
   const int teams = grid * (warps >> p.lt);
   p.share = (int)(((int64_t)p.total + teams - 1) / teams);
@@ -1086,10 +1097,14 @@ struct Split {
   int nqb, qper, may_cut;
 };
 
-Split split_of(int page, int kv_heads, int q_heads, int max_pages) {
+// Queries a pass over the cache: eight, or four of 256 dimensions (a warp's sums are its registers'
+// bound; eight took 255 of them, with spills, and ran 35.0 us where two passes take 33.8, the second
+// mostly from L2).
+
+Split split_of(int page, int dim, int kv_heads, int q_heads, int max_pages) {
   Split s;
-  const int group = q_heads / kv_heads;
-  s.nqb = (group + kQ - 1) / kQ;
+  const int group = q_heads / kv_heads, most = dim == kGroup ? kQ : kQ / 2;
+  s.nqb = (group + most - 1) / most;
   s.qper = (group + s.nqb - 1) / s.nqb;
   s.may_cut = (int64_t)max_pages * page > kWholeTiles * kTile;
   return s;
@@ -1105,7 +1120,7 @@ unsigned take_attn_error() {
 }
 
 size_t attn_workspace_bytes(const qlin_kv_desc* d, int q_heads, int, int max_pages) {
-  const Split s = split_of(d->page_size, d->kv_heads, q_heads, max_pages);
+  const Split s = split_of(d->page_size, d->head_dim, d->kv_heads, q_heads, max_pages);
   if (!s.may_cut) return 0;
   return kRecordBytes + (size_t)kMaxTeams * 2 * s.qper * (d->head_dim + 4) * sizeof(float);
 }
@@ -1113,7 +1128,7 @@ size_t attn_workspace_bytes(const qlin_kv_desc* d, int q_heads, int, int max_pag
 qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_stride, int q_heads,
                                const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
                                const uint32_t* sign_bits, float scale, __half* out, void* workspace, cudaStream_t s) {
-  const Split sp = split_of(c.page, c.heads, q_heads, max_pages);
+  const Split sp = split_of(c.page, c.dim, c.heads, q_heads, max_pages);
   AttnArgs a;
   a.c = c;
   a.q = q;
@@ -1136,8 +1151,8 @@ qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_strid
   a.nqb = sp.nqb;
   a.qper = sp.qper;
   a.may_cut = sp.may_cut;
-  if (sp.qper > 4) return c.dim == kGroup ? launch_widths<1, 2>(a, s) : launch_widths<2, 2>(a, s);
-  return c.dim == kGroup ? launch_widths<1, 1>(a, s) : launch_widths<2, 1>(a, s);
+  if (c.dim != kGroup) return launch_widths<2, 1>(a, s);
+  return sp.qper > 4 ? launch_widths<1, 2>(a, s) : launch_widths<1, 1>(a, s);
 }
 
 }  // namespace qlin

@@ -17,7 +17,7 @@
 namespace qlin {
 
 constexpr int kPageUnit = 16;  // tokens: pages are multiples of this, tiles never cross a page
-constexpr int kItemExtra = 32; // most that attention adds to an item's tiles when it deals them out
+constexpr int kItemExtra = 36; // most that attention adds to an item's tiles when it deals them out
 
 struct KvView {
   uint8_t* pool;
