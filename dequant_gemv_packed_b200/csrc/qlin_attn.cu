@@ -171,8 +171,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
     // the longest item on one team, or all items on all warps, in tiles of a warp: the least
     int best = 0x7fffffff;
     for (int lt = p.lt; lt >= 0; --lt) {
-      const int e = item_extra(lt), all = (int)(((int64_t)n * a.items + (int64_t)live * e) / (grid * warps));
-      const int cost = max((top + e) >> lt, all);
+      const int e = item_extra(lt), cost = max((top + e) >> lt, div_pos(n * a.items + live * e, grid * warps));
       if (cost < best) best = cost, p.lt = lt;
     }
   }
@@ -180,7 +179,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
   static_assert(4 + 4 * warps <= kItemExtra, "positions are counted in an int");
   p.total = n * a.items + live * p.extra;
   const int teams = grid * (warps >> p.lt);
-  p.share = (int)(((int64_t)p.total + teams - 1) / teams);
+  p.share = div_pos(p.total, teams) + 1;
   p.share = max(p.share, p.cut ? kMinShare : 1);
   return p;
 }
@@ -188,6 +187,8 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
 // The sequence that position u (< total) belongs to, and its first position.
 __device__ __forceinline__ void find_pos(const AttnArgs& a, const Plan& p, const int* lens, int lane, int u,
                                          int& b, int& first) {
+  b = first = 0;
+  if (a.batch == 1) return;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const int t = b0 + lane < a.batch ? tiles_in(len_of(a, lens, b0 + lane)) : 0;
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     find_pos(a, plan, lens, lane, cur.x, cur.y, cur.z);
     cur.w = tiles_in(len_of(a, lens, cur.y));
     if (!plan.cut) {  // items that start in the share
-      const int cost = cur.w + plan.extra, at = (cur.x - cur.z) % cost;
+      const int cost = cur.w + plan.extra, at = cur.x - cur.z - div_pos(cur.x - cur.z, cost) * cost;
       if (at) cur.x += cost - at;
     }
     more = next_segment(a, plan, lens, cur, end, seg);
