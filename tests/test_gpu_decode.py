@@ -433,6 +433,158 @@ def test_captured_step_follows_new_inputs():
         check_attention(ref, held, tq.cpu().numpy(), table, new, sb=sb, what=str(new))
 
 
+def test_many_sequences():
+    """More sequences than a block keeps lengths of (512), empty ones among them, in small pages."""
+    rng = np.random.default_rng(31)
+    B = 700
+    lens = rng.integers(0, 40, B)
+    lens[[0, 5, 511, 512, 699]] = 0, 37, 16, 39, 0
+    c = filled(rng, 60, 16, 1, 128, 8, 4, None)
+    table = rng.integers(0, 60, (B, 3))  # sequences may share pages
+    q = rng.standard_normal((B, 2, 128)).astype(np.float16)
+    check_attention(run_attention(c, q, table, lens), c, q, table, lens)
+
+
+@pytest.mark.parametrize("dim,heads,group,kb,vb", [(128, 5, 3, 4, 8), (256, 1, 16, 8, 8), (128, 2, 16, 16, 16),
+                                                   (256, 3, 3, 16, 16), (128, 1, 7, 8, 8)])
+def test_long_among_short(dim, heads, group, kb, vb):
+    """Two long sequences cut over many teams, between scores of short ones of every tile count."""
+    rng = np.random.default_rng(heads * group)
+    lens = [3, 1900, 16, 17, 0, 1, 1000, 512, 513, 528] + list(range(1, 120, 7))
+    width = 60
+    c = filled(rng, 90, 32, heads, dim, kb, vb, None)
+    table = rng.integers(0, 90, (len(lens), width))
+    q = (1.5 * rng.standard_normal((len(lens), heads * group, dim))).astype(np.float16)
+    check_attention(run_attention(c, q, table, lens), c, q, table, lens)
+
+
+@pytest.mark.parametrize("n", [496, 511, 512, 513, 529])
+def test_the_border_of_cutting(n):
+    """Tables and lengths on both sides of the longest item that is not cut (512 tokens)."""
+    rng = np.random.default_rng(n)
+    c = filled(rng, 34, 16, 1, 128, 8, 8, None)
+    q = rng.standard_normal((2, 4, 128)).astype(np.float16)
+    for width in (32, 34):
+        table = rng.permutation(34)[None, :width].repeat(2, 0)
+        lens = [min(n, width * 16), 20]
+        check_attention(run_attention(c, q, table, lens), c, q, table, lens, what=f"{n} in {width} pages")
+
+
+@pytest.mark.parametrize("kb", [4, 8])
+def test_query_with_an_outlying_channel(kb):
+    """A query channel 2,000 times the others: their 16-bit integers are few, within the bound."""
+    rng = np.random.default_rng(32)
+    c = filled(rng, 8, 16, 1, 128, kb, 8, None)
+    q = (0.05 * rng.standard_normal((1, 4, 128))).astype(np.float16)
+    q[0, :, 7] = 100
+    table = np.arange(8)[None]
+    check_attention(run_attention(c, q, table, [128]), c, q, table, [128])
+
+
+def test_workspace_contents_do_not_matter():
+    c, q, table, lens, sb = long_case(33)
+    ref = run_attention(c, q, table, lens, sb=sb)
+    size = Q.qlin_attn_workspace_bytes(kv_desc(c), 8, 3, table.shape[1])
+    assert size > 0
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+    pool = pool_of(c)
+    for fill in (0xFF, 0x01, None):
+        if fill is not None:
+            ws.fill_(fill)
+        assert torch.equal(run_attention(c, q, table, lens, sb=sb, pool=pool, workspace=ws), ref)
+    with pytest.raises(Q.QlinError, match="WORKSPACE"):
+        run_attention(c, q, table, lens, sb=sb, pool=pool, workspace=ws[:size - 16])
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured: nothing is set up outside the graph."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+from dequant_gemv_packed_b200 import qlin as Q
+d = Q.KVDesc(80, 16, 1, 128, 8, 4)
+pool = torch.zeros(Q.qlin_kv_cache_bytes(d), dtype=torch.uint8, device="cuda")
+k = torch.randn(900, 1, 128, device="cuda").half()
+slots = torch.arange(900, device="cuda", dtype=torch.int32)
+q = torch.randn(1, 4, 128, device="cuda").half()
+table = torch.arange(80, device="cuda", dtype=torch.int32).view(1, 80)
+n = torch.tensor([900], device="cuda", dtype=torch.int32)
+w = torch.ones(512, device="cuda").half()
+def step():
+    Q.qlin_kv_write(d, pool, k, k, slots)
+    o = Q.qlin_attn_decode(d, pool, q, table, n)
+    return o, Q.qlin_rmsnorm(o.view(1, 512), w, 1e-6), Q.qlin_kv_read(d, pool, slots)[1]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, step())) and outs[0].abs().max() > 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_binding_refuses_wrong_tensors():
+    """Shapes, types and layouts that the binding checks before a call."""
+    rng = np.random.default_rng(34)
+    c = filled(rng, 4, 16, 2, 128, 8, 8, None)
+    d, pool = kv_desc(c), pool_of(c)
+    q = torch.zeros(2, 4, 128, device=DEV).half()
+    table, lens = torch.zeros(2, 2, device=DEV, dtype=torch.int32), torch.zeros(2, device=DEV, dtype=torch.int32)
+    k, slots = torch.zeros(3, 2, 128, device=DEV).half(), torch.zeros(3, device=DEV, dtype=torch.int32)
+    sb = torch.zeros(8, device=DEV, dtype=torch.int32)
+    bad = [(TypeError, lambda: Q.qlin_attn_decode(d, pool, q.float(), table, lens)),
+           (TypeError, lambda: Q.qlin_attn_decode(d, pool, q, table.long(), lens)),
+           (TypeError, lambda: Q.qlin_attn_decode(d, pool, q, table, lens.cpu())),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool, q, table[:1], lens)),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool, q, table, lens[:1])),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool, q[0], table, lens)),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool, q.transpose(1, 2).contiguous().transpose(1, 2), table, lens)),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool, q, table, lens, out=q[:1].clone())),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool, q, table, lens, sign_bits=sb)),
+           (ValueError, lambda: Q.qlin_attn_decode(d, pool[:-16], q, table, lens)),
+           (Q.QlinError, lambda: Q.qlin_attn_decode(d, pool, q[:, :3], table, lens)),
+           (Q.QlinError, lambda: Q.qlin_attn_decode(d, pool, q, table, lens, out=q)),
+           (Q.QlinError, lambda: Q.qlin_attn_decode(d, pool, q[:0], table[:0], lens[:0])),
+           (TypeError, lambda: Q.qlin_kv_write(d, pool, k.float(), k, slots)),
+           (ValueError, lambda: Q.qlin_kv_write(d, pool, k[:, :1], k, slots)),
+           (ValueError, lambda: Q.qlin_kv_write(d, pool, k, k[:2], slots)),
+           (ValueError, lambda: Q.qlin_kv_write(d, pool, k, k, slots[:2])),
+           (Q.QlinError, lambda: Q.qlin_kv_write(d, pool, k[:1].expand(3, 2, 128), k, slots)),
+           (TypeError, lambda: Q.qlin_kv_read(d, pool, slots.float())),
+           (ValueError, lambda: Q.qlin_kv_read(d, pool, slots, k=k[:2])),
+           (Q.QlinError, lambda: Q.qlin_kv_read(d, pool, slots, k=k, v=k)),
+           (ValueError, lambda: Q.qlin_rmsnorm(k.view(3, 256), k.view(3, 256)[0, :128], 1e-6)),
+           (ValueError, lambda: Q.qlin_rmsnorm(k.view(3, 256), k.view(3, 256)[0], 1e-6, residual_out=k.view(3, 256).clone())),
+           (Q.QlinError, lambda: Q.qlin_rmsnorm(k.view(3, 256), k.view(3, 256)[0].clone(), -1.0))]
+    for kind, call in bad:
+        with pytest.raises(kind):
+            call()
+
+
+def test_write_and_read_many_tokens():
+    """More units than the grid has lanes for: every block walks on; odd heads and two groups a head."""
+    rng = np.random.default_rng(35)
+    for heads, dim, t in ((3, 128, 4300), (1, 256, 5000)):
+        c = D.Cache(-(-t // 48) + 1, 48, heads, dim, 8, 4)
+        slots = rng.permutation(c.bytes.shape[0] * 48)[:t].astype(np.int32)
+        slots[::97] = -1
+        sb = signs(rng, dim)
+        k, v = vectors(rng, t, heads, dim), vectors(rng, t, heads, dim)
+        d, pool = kv_desc(c), pool_of(c)
+        Q.qlin_kv_write(d, pool, dev(k), dev(v), dev(slots), sign_bits=dev(sb))
+        c.write(k, v, slots, sb)
+        assert np.array_equal(pool.cpu().numpy().reshape(c.bytes.shape), c.bytes)
+        for g, r in zip(Q.qlin_kv_read(d, pool, dev(slots), sign_bits=dev(sb)), c.read(slots, sb)):
+            assert np.array_equal(g.cpu().numpy(), r)
+
+
 # ----------------------------------------------------------------------- norm
 
 def check_norm(x, w, eps, res=None, **kw):
@@ -450,7 +602,8 @@ def check_norm(x, w, eps, res=None, **kw):
 
 @pytest.mark.parametrize("res", [False, True])
 @pytest.mark.parametrize("M,K", [(1, 8), (3, 136), (5, 1000), (1, 1024), (2, 1032), (1, 2560), (7, 2560), (300, 2568),
-                                 (2, 8192), (3, 9728), (2, 16392), (2, 65536), (1000, 128)])
+                                 (2, 8192), (3, 9728), (2, 16392), (2, 40000), (2, 65536), (1000, 128),
+                                 (70001, 64)])
 def test_norm(M, K, res):
     rng = np.random.default_rng(M + K)
     x = (rng.standard_normal((M, K)) * np.exp(rng.standard_normal((M, 1)))).astype(np.float16)
