@@ -23,6 +23,8 @@ def _built():
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
     Q.lib()
+    yield
+    torch.cuda.empty_cache()  # some cases fill gigabytes, and some fill them with NaN
 
 
 @pytest.fixture(autouse=True)
