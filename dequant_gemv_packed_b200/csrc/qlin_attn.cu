@@ -524,7 +524,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   uint8_t* const ring_ptr = smem + warp * S * C::kStage;
   const uint32_t ring = smem_addr(ring_ptr);
 
-  if (a.may_cut && threadIdx.x == 0) grid_launch_dependents();
+  grid_launch_dependents();
+  grid_dependency_wait();
   __shared__ int lens[kLensCached];
   __shared__ uint32_t signs[4 * NG];
   if (a.sign_bits && threadIdx.x < 4 * NG) signs[threadIdx.x] = a.sign_bits[threadIdx.x];
@@ -1007,6 +1008,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   __shared__ __align__(16) float sums[NG][kJoinWarps][kGroup];
   __shared__ float2 sml[NG][kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = blockIdx.y, c0 = blockIdx.x;
+  grid_launch_dependents();
   grid_dependency_wait();  // every block: this grid's end stands for the first one's too
   const int4 rec = __ldcg(a.records + c0);
   if (q >= rec.y) return;
@@ -1072,19 +1074,9 @@ qlin_status launch(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return record_cuda(e);
     if (dev < 64) configured.fetch_or(1ull << dev, std::memory_order_release);
   }
-  attn_kernel<KB, VB, NG, NT><<<C::kGrid, C::kWarps * 32, C::kSmem, s>>>(a);
-  const qlin_status r = record_cuda(cudaGetLastError());
+  const qlin_status r = launch_dependent(attn_kernel<KB, VB, NG, NT>, C::kGrid, C::kWarps * 32, C::kSmem, s, a);
   if (r != QLIN_OK || !a.may_cut) return r;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C::kGrid - 1, a.qper);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return record_cuda(cudaLaunchKernelEx(&cfg, attn_join_kernel<NG>, a));
+  return launch_dependent(attn_join_kernel<NG>, dim3(C::kGrid - 1, a.qper), kJoinWarps * 32, 0, s, a);
 }
 
 template <int NG, int NT>

@@ -36,6 +36,25 @@ PackedView make_view(const qlin_desc* d, const void* packed);
 qlin_status record_cuda(cudaError_t e);
 bool overlap_enabled();
 
+// Launches a kernel as a programmatic dependent of the one before it on the stream: it may be set up
+// while that one ends, and its first statement must be grid_dependency_wait() (qlin_sm100.cuh), after
+// which everything is as in an ordinary launch.
+template <typename... Params, typename... Args>
+qlin_status launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return record_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 // Launchers (each returns QLIN_OK or QLIN_ERR_CUDA).
 qlin_status launch_pack(const PackedView& v, const uint8_t* codes, uint8_t* packed,
                         cudaStream_t s);

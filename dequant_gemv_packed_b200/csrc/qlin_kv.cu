@@ -25,6 +25,7 @@
 // so the rest is written in two-value operations (reading 30,001 rotated tokens of 8
 // heads took 574 instructions a warp and 84 us before, HBM's share being 26 us).
 #include "qlin_kv.cuh"
+#include "qlin_sm100.cuh"
 
 namespace qlin {
 namespace {
@@ -112,6 +113,8 @@ __device__ __forceinline__ int checked_slot(const KvArgs& a, int s, int t) {
 // The loops below keep the next unit's data and the slot of the one after it in flight.
 
 __global__ void __launch_bounds__(kThreads, kCtas) kv_write_kernel(const __grid_constant__ KvArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Walk w(a, lane, warp);
   const int64_t stride = w.side ? a.v_stride : a.k_stride;
@@ -220,6 +223,8 @@ __device__ __forceinline__ f32x2 dequant2(uint32_t a, uint32_t b, f32x2 inv_unit
 }
 
 __global__ void __launch_bounds__(kThreads, kCtas) kv_read_kernel(const __grid_constant__ KvArgs a) {
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Walk w(a, lane, warp);
   const int64_t stride = (int64_t)a.c.heads * a.c.dim;
@@ -323,8 +328,7 @@ qlin_status launch_kv_write(const KvView& c, const __half* k, const __half* v, i
   unsigned grid;
   const qlin_status r = kv_grid(a, &grid);
   if (r != QLIN_OK) return r;
-  kv_write_kernel<<<grid, kThreads, 0, s>>>(a);
-  return record_cuda(cudaGetLastError());
+  return launch_dependent(kv_write_kernel, grid, kThreads, 0, s, a);
 }
 
 qlin_status launch_kv_read(const KvView& c, __half* k, __half* v, const int32_t* slots, int tokens,
@@ -333,8 +337,7 @@ qlin_status launch_kv_read(const KvView& c, __half* k, __half* v, const int32_t*
   unsigned grid;
   const qlin_status r = kv_grid(a, &grid);
   if (r != QLIN_OK) return r;
-  kv_read_kernel<<<grid, kThreads, 0, s>>>(a);
-  return record_cuda(cudaGetLastError());
+  return launch_dependent(kv_read_kernel, grid, kThreads, 0, s, a);
 }
 
 }  // namespace qlin

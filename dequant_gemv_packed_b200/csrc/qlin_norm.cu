@@ -5,6 +5,7 @@
 // 16-byte pieces (64 values) a lane.  Bound by HBM: x and the residual in, y and
 // the residual out, each once.
 #include "qlin_internal.cuh"
+#include "qlin_sm100.cuh"
 
 namespace qlin {
 namespace {
@@ -40,6 +41,8 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 // One row a block (blockDim.y = 1) or a warp (blockDim.x = 32); NP pieces a thread.
 template <int NP, bool kResidual>
 __global__ void __launch_bounds__(kMaxWarps * 32) rmsnorm_kernel(const NormArgs a) {
+  grid_launch_dependents();  // a dependent (a GEMV that overlaps) may fetch its weights meanwhile
+  grid_dependency_wait();
   __shared__ float part[kMaxWarps];
   const int row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= a.rows) return;  // whole warps: blocks of several rows have one warp each
@@ -109,22 +112,20 @@ qlin_status launch(const NormArgs& a, cudaStream_t s) {
     const dim3 block(32, 4);
     const unsigned grid = (unsigned)((a.rows + 3) / 4);
     if (a.pieces <= 32)
-      rmsnorm_kernel<1, kResidual><<<grid, block, 0, s>>>(a);
+      return launch_dependent(rmsnorm_kernel<1, kResidual>, grid, block, 0, s, a);
     else if (a.pieces <= 64)
-      rmsnorm_kernel<2, kResidual><<<grid, block, 0, s>>>(a);
+      return launch_dependent(rmsnorm_kernel<2, kResidual>, grid, block, 0, s, a);
     else
-      rmsnorm_kernel<4, kResidual><<<grid, block, 0, s>>>(a);
-    return record_cuda(cudaGetLastError());
+      return launch_dependent(rmsnorm_kernel<4, kResidual>, grid, block, 0, s, a);
   }
   const unsigned grid = (unsigned)a.rows;
   const auto threads = [&](int np) { return dim3((unsigned)(((a.pieces + np - 1) / np + 31) / 32 * 32)); };
   if (a.pieces <= 2048)
-    rmsnorm_kernel<2, kResidual><<<grid, threads(2), 0, s>>>(a);
+    return launch_dependent(rmsnorm_kernel<2, kResidual>, grid, threads(2), 0, s, a);
   else if (a.pieces <= 4096)
-    rmsnorm_kernel<4, kResidual><<<grid, threads(4), 0, s>>>(a);
+    return launch_dependent(rmsnorm_kernel<4, kResidual>, grid, threads(4), 0, s, a);
   else
-    rmsnorm_kernel<8, kResidual><<<grid, threads(8), 0, s>>>(a);
-  return record_cuda(cudaGetLastError());
+    return launch_dependent(rmsnorm_kernel<8, kResidual>, grid, threads(8), 0, s, a);
 }
 
 }  // namespace
