@@ -169,9 +169,12 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
   p.lt = 31 - __clz(warps);
   if (!p.cut) {
     // the longest item on one team, or all items on all warps, in tiles of a warp: the least
-    int best = 0x7fffffff;
-    for (int lt = p.lt; lt >= 0; --lt) {
-      const int e = item_extra(lt), cost = max((top + e) >> lt, div_pos(n * a.items + live * e, grid * warps));
+    const float per_warp = rcp((float)(grid * warps));
+    float best = INFINITY;
+#pragma unroll
+    for (int lt = 31 - __builtin_clz(warps); lt >= 0; --lt) {
+      const int e = item_extra(lt);
+      const float cost = fmaxf((float)(top + e) / (float)(1 << lt), (float)(n * a.items + live * e) * per_warp);
       if (cost < best) best = cost, p.lt = lt;
     }
   }
@@ -179,7 +182,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
   static_assert(4 + 4 * warps <= kItemExtra, "positions are counted in an int");
   p.total = n * a.items + live * p.extra;
   const int teams = grid * (warps >> p.lt);
-  p.share = div_pos(p.total, teams) + 1;
+  p.share = (int)((float)p.total * rcp((float)teams)) + 1 + (p.total >> 21);  // teams * share >= total
   p.share = max(p.share, p.cut ? kMinShare : 1);
   return p;
 }
@@ -189,10 +192,29 @@ __device__ __forceinline__ void find_pos(const AttnArgs& a, const Plan& p, const
                                          int& b, int& first) {
   b = first = 0;
   if (a.batch == 1) return;
-  int before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int t = b0 + lane < a.batch ? tiles_in(len_of(a, lens, b0 + lane)) : 0;
-    const int n = t ? (t + p.extra) * a.items : 0;
+  const auto cost = [&](int i) {
+    const int t = i < a.batch ? tiles_in(len_of(a, lens, i)) : 0;
+    return t ? (t + p.extra) * a.items : 0;
+  };
+  // the lane whose run of sequences holds u, then 32 of that run at a time
+  int before = 0, from = 0, to = a.batch;
+  if (a.batch > 32) {
+    const int run = (a.batch + 31) / 32;
+    int n = 0;
+    for (int i = 0; i < run; ++i) n += cost(lane * run + i);
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const int l = __ffs(__ballot_sync(0xffffffffu, sum > u)) - 1;  // u < total: there is one
+    before = __shfl_sync(0xffffffffu, sum - n, l);
+    from = l * run;
+    to = from + run;
+  }
+  for (int b0 = from; b0 < to; b0 += 32) {
+    const int n = b0 + lane < to ? cost(b0 + lane) : 0;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -44,8 +44,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) rmsnorm_kernel(const NormArgs 
   grid_launch_dependents();  // a dependent (a GEMV that overlaps) may fetch its weights meanwhile
   grid_dependency_wait();
   __shared__ float part[kMaxWarps];
-  const int row = blockIdx.x * blockDim.y + threadIdx.y;
-  if (row >= a.rows) return;  // whole warps: blocks of several rows have one warp each
+  const unsigned row = blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= (unsigned)a.rows) return;  // whole warps: blocks of several rows have one warp each
   const int64_t base = (int64_t)row * a.pieces;
   uint4 h[NP], r[NP], w[NP];
 #pragma unroll
@@ -110,7 +110,7 @@ qlin_status launch(const NormArgs& a, cudaStream_t s) {
   // (8 lines in flight each) until the block is full.
   if (a.pieces <= 128) {
     const dim3 block(32, 4);
-    const unsigned grid = (unsigned)((a.rows + 3) / 4);
+    const unsigned grid = ((unsigned)a.rows + 3) / 4;
     if (a.pieces <= 32)
       return launch_dependent(rmsnorm_kernel<1, kResidual>, grid, block, 0, s, a);
     else if (a.pieces <= 64)

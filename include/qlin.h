@@ -441,7 +441,8 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  * as 16-bit integers with one power-of-two scale per group of 128 (exact for values
  * within a factor 8 of the group's largest, others rounded at 2^-14 of it, far
  * below half a step of the keys); the softmax weights enter the value sums with 22
- * bits.  Deterministic.
+ * bits.  An infinity or NaN among a head's query, keys or values within the length
+ * gives NaN there; what lies past the length has no effect.  Deterministic.
    q     : device fp16, sequence b's heads [q_heads][head_dim] at element offset
  *           b * q_stride; q_stride >= q_heads * head_dim, a multiple of 8;
  *           q_heads a multiple of kv_heads;
