@@ -19,19 +19,28 @@
 // the exponent, P_t = 2^(score_t + log2 s_v - m) = w_t s_v, so that
 //   out_d = (sum_t P_t q_v - z_v P_t) / sum_t P_t / s_v,
 // and m follows the maximum of score + log2 s_v: P is the weight that the sum is
-// really made of, whatever the sizes of the scales.  P enters the products as two
-// fp16 digits, hi + 2^-11 lo (22 bits).  m is kept 7 to 15 binary orders below the
-// maximum and moved only when a score exceeds it by 15, which a vote decides: after
-// the first tile that is rare.
+// really made of, whatever the sizes of the scales.  m is kept 7 to 15 binary orders
+// below the maximum and moved only when a score exceeds it by 15, which a vote
+// decides: after the first tile that is rare.
 //
-// The columns of both products are (query, digit) pairs, four queries in eight
-// columns: lane (g, t) of an accumulator holds both digits of query t, so each lane
-// has the scores of one query for tokens g and g + 8 (none is padding at the usual
-// four queries a key), packs (hi, lo) of P as it is, and movmatrix turns that into
-// the next product's operand; a query's statistics live in the lanes that scale its
-// sums.  S^T = K Q^T has the tile's 16 tokens as rows, O^T = V^T P^T 16 dimensions.
-// More than four queries take a second set of columns on the same decoded codes
-// (NT = 2), more than eight (four of 256 dimensions) another pass over the cache.
+// The eight columns of the products.  S^T = K Q^T has the tile's 16 tokens as rows,
+// O^T = V^T P^T 16 dimensions; lane (g, t) of an accumulator has columns 2t, 2t + 1.
+// Up to four queries (NT = 1): the columns are (query, digit) pairs in both, so a
+// lane has the scores of query t for tokens g and g + 8 (none is padding at the usual
+// four queries a key), and P enters the value sums as two fp16 digits, hi + 2^-11 lo
+// (22 bits), packed as they are.
+// Five to eight queries (NT = 2): the keys' products take a second set of (query,
+// digit) columns (16-bit keys: one set of eight queries), with queries 2t and 2t + 1
+// in lane t, and the columns of the value sums are the eight queries: P is one fp16
+// number.  Its rounding, 2^-12 of a weight, stands in the zero's share and the
+// denominator too, so that it moves the weights and not their normalisation (a
+// subnormal P, 2^21 below the largest, enters the denominator unrounded: a token with
+// a tiny scale may hold most of the weight).  A second digit would need a second set of
+// sums: half the warps an SM, and twice the value products (24 x 9000 tokens of 8 kv
+// heads at 4 bits: 76.7 us with it, 68.2 without).
+// In both movmatrix turns the packed pair into the next product's operand, and a
+// query's statistics live in the lanes that scale its sums.  More than eight queries
+// take another pass over the cache.
 //
 // Split.  A tile is 16 tokens of one (sequence, kv head, block of queries), an item
 // all tiles of one.  Items in order, each its tiles plus a constant for what an item
@@ -90,17 +99,17 @@ struct Cfg {
   // and a word: the tile's tokens; multiples of the longest row, so that swizzles apply to addresses
   static constexpr int kAlign = KB == 16 ? 256 : 128;
   static constexpr int kStage = ((kTileBytes > kDump ? kTileBytes : kDump) + 16 + kAlign - 1) / kAlign * kAlign;
-  // 32 accumulators a warp (one group, four queries) leave room for 16 warps an SM at 128
-  // registers; 64 (two groups, or eight queries) for 12 at 168.  16-bit rows fill the rings: 8 warps.
-  static constexpr int kSets = NG * NT;
-  static_assert(kSets <= 2, "registers");
+  // 32 sums a lane (one group) leave room for 16 warps an SM at 128 registers; 64 (two) for 12 at
+  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 31.0 us; at 168 with
+  // spills 44.1, two passes of four queries 33.0).  16-bit rows fill the rings: 8 warps.
+  static constexpr int kSets = NG;
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
   static constexpr int kSmemQ = kWarps * NT * NG * 1024;        // operand of the queries, a team
   static constexpr int kSmemX = kWarps * kRowQ * NG * 8;        // (scale, sum) of each, a team
   static constexpr int kSmemMl = kWarps * 4 * 8;                // (m, l) of four queries, a warp
   static constexpr int kOther = kSmemQ + kSmemX + kSmemMl + kAlign;  // and room to align it
   static constexpr int fit(int ctas) { return (226 * 1024 / ctas - 4096 - kOther) / (kWarps * kStage); }
-  static constexpr int kCtas = kSets == 2 && KB < 16 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;  // per SM
+  static constexpr int kCtas = kSets == 2 && NT == 1 && KB < 16 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;  // per SM
   static constexpr int kStages = fit(kCtas) > 6 ? 6 : fit(kCtas);
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kSmem = kRing + kOther;
@@ -703,40 +712,45 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     }
     team_barrier();
     constexpr int NB = KB == 16 ? 16 : 8;  // operand registers a group
-    uint32_t qf[NT][NG][NB];
-    float xs[NT][NG], sc[NT][NG];  // sum and scale of query t4
+    constexpr int NS = KB == 16 ? 1 : NT;  // column sets of the keys' products
+    uint32_t qf[NS][NG][NB];
+    float xs[NT][NG], sc[NT][NG];  // sum and scale of query(s, t4)
+    const auto query = [](int s, int t) { return NT == 1 ? t : 2 * t + s; };
 #pragma unroll
     for (int s = 0; s < NT; ++s)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint32_t base = smem_addr(sq);
+        if (s < NS) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (KB == 16) {  // piece t4 + 4 j of query g8 / 2; the odd columns are zero
-            uint4 p = ld128(base + ((4 * s + (g8 >> 1)) * D + g * kGroup + 32 * j + 8 * t4) * 2);
-            if (g8 & 1) p = make_uint4(0u, 0u, 0u, 0u);
-            qf[s][g][(4 * j) % NB] = p.x, qf[s][g][(4 * j + 1) % NB] = p.y;
-            qf[s][g][(4 * j + 2) % NB] = p.z, qf[s][g][(4 * j + 3) % NB] = p.w;
-          } else {  // eight dimensions: 4 bits, word j of piece t4; 8 bits, words 2 (j & 1), + 1 of piece t4 + 4 (j / 2)
-            const int d0 = KB == 4 ? 32 * t4 + 8 * j : 64 * (j >> 1) + 16 * t4 + 8 * (j & 1);
-            const uint2 p = ld64(base + (8 * s + g8) * D + g * kGroup + d0);
-            qf[s][g][2 * j] = p.x, qf[s][g][2 * j + 1] = p.y;
+          for (int j = 0; j < 4; ++j) {
+            if (KB == 16) {  // piece t4 + 4 j of query g8 / 2 (the odd columns are zero), or of query g8
+              uint4 p = ld128(base + ((NT == 1 ? g8 >> 1 : g8) * D + g * kGroup + 32 * j + 8 * t4) * 2);
+              if (NT == 1 && (g8 & 1)) p = make_uint4(0u, 0u, 0u, 0u);
+              qf[s % NS][g][(4 * j) % NB] = p.x, qf[s % NS][g][(4 * j + 1) % NB] = p.y;
+              qf[s % NS][g][(4 * j + 2) % NB] = p.z, qf[s % NS][g][(4 * j + 3) % NB] = p.w;
+            } else {  // eight dimensions: 4 bits, word j of piece t4; 8 bits, words 2 (j & 1), + 1 of piece t4 + 4 (j / 2)
+              const int d0 = KB == 4 ? 32 * t4 + 8 * j : 64 * (j >> 1) + 16 * t4 + 8 * (j & 1);
+              const uint2 p = ld64(base + (2 * query(s, g8 >> 1) + (g8 & 1)) * D + g * kGroup + d0);
+              qf[s % NS][g][2 * j] = p.x, qf[s % NS][g][2 * j + 1] = p.y;
+            }
           }
         }
-        const float2 x = sx[(4 * s + t4) * NG + g];
+        const float2 x = sx[query(s, t4) * NG + g];
         sc[s][g] = x.x, xs[s][g] = x.y;
       }
 
-    float o[NT][NG][8][4], m[NT][NG], l[NT][NG], zc[NT][NG];
+    float o[NG][8][4], m[NT][NG], l[NT][NG], zc[NT][NG];
 #pragma unroll
-    for (int s = 0; s < NT; ++s)
+    for (int g = 0; g < NG; ++g) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int j = 0; j < 8; ++j) o[g][j][0] = o[g][j][1] = o[g][j][2] = o[g][j][3] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[s][g][j][0] = o[s][g][j][1] = o[s][g][j][2] = o[s][g][j][3] = 0.f;
+      for (int s = 0; s < NT; ++s) {
         m[s][g] = kNone;
         l[s][g] = zc[s][g] = 0.f;
       }
+    }
 
     for (int k = 0; k < cnt; ++k) {
       cp_wait<S - 2>();
@@ -747,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
       const uint32_t st = ring + stage;
       const int valid = *reinterpret_cast<const volatile int*>(ring_ptr + stage + C::kStage - 16);
 
-      // scores in units of log2: query t4 (+ 4 s), tokens g8 and g8 + 8
+      // scores in units of log2: query(s, t4), tokens g8 and g8 + 8
       float w[NT][2];
       float lv[NG][2], rv[NG][2], vz[NG][2];
 #pragma unroll
@@ -769,9 +783,9 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             constexpr uint32_t lo = 0x0F0F0F0Fu, hi = 0xF0F0F0F0u;
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
-              imma(c0[s], ra[j] & lo, rb[j] & lo, ra[j + 1] & lo, rb[j + 1] & lo, qf[s][g][2 * j], qf[s][g][2 * j + 2]);
-              imma(c1[s], ra[j] & hi, rb[j] & hi, ra[j + 1] & hi, rb[j + 1] & hi, qf[s][g][2 * j + 1],
-                   qf[s][g][2 * j + 3]);
+              imma(c0[s], ra[j] & lo, rb[j] & lo, ra[j + 1] & lo, rb[j + 1] & lo, qf[s % NS][g][2 * j], qf[s % NS][g][2 * j + 2]);
+              imma(c1[s], ra[j] & hi, rb[j] & hi, ra[j + 1] & hi, rb[j + 1] & hi, qf[s % NS][g][2 * j + 1],
+                   qf[s % NS][g][2 * j + 3]);
             }
           }
 #pragma unroll
@@ -790,8 +804,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const uint4 wa = ld128(kb ^ (64 * j)), wb = ld128((kb ^ (64 * j)) + 128 * KB);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
-              imma(c0[s], wa.x, wb.x, wa.y, wb.y, qf[s][g][4 * j], qf[s][g][4 * j + 1]);
-              imma(c1[s], wa.z, wb.z, wa.w, wb.w, qf[s][g][4 * j + 2], qf[s][g][4 * j + 3]);
+              imma(c0[s], wa.x, wb.x, wa.y, wb.y, qf[s % NS][g][4 * j], qf[s % NS][g][4 * j + 1]);
+              imma(c1[s], wa.z, wb.z, wa.w, wb.w, qf[s % NS][g][4 * j + 2], qf[s % NS][g][4 * j + 3]);
             }
           }
 #pragma unroll
@@ -800,24 +814,17 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             for (int i = 0; i < 2; ++i)
               dot[s][i] = (float)((c0[s][2 * i] + c1[s][2 * i]) * 256 + (c0[s][2 * i + 1] + c1[s][2 * i + 1]));
         } else {
-          float c0[NT][4], c1[NT][4];
-#pragma unroll
-          for (int s = 0; s < NT; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c0[s][i] = c1[s][i] = 0.f;
+          float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 wa = ld128(kb ^ (64 * j)), wb = ld128((kb ^ (64 * j)) + 128 * KB);
-#pragma unroll
-            for (int s = 0; s < NT; ++s) {
-              mma(c0[s], wa.x, wb.x, wa.y, wb.y, qf[s][g][(4 * j) % NB], qf[s][g][(4 * j + 1) % NB]);
-              mma(c1[s], wa.z, wb.z, wa.w, wb.w, qf[s][g][(4 * j + 2) % NB], qf[s][g][(4 * j + 3) % NB]);
-            }
+            mma(c0, wa.x, wb.x, wa.y, wb.y, qf[0][g][(4 * j) % NB], qf[0][g][(4 * j + 1) % NB]);
+            mma(c1, wa.z, wb.z, wa.w, wb.w, qf[0][g][(4 * j + 2) % NB], qf[0][g][(4 * j + 3) % NB]);
           }
 #pragma unroll
           for (int s = 0; s < NT; ++s)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) dot[s][i] = c0[s][2 * i] + c1[s][2 * i];
+            for (int i = 0; i < 2; ++i) dot[s][i] = c0[2 * i + s] + c1[2 * i + s];
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // tokens g8, g8 + 8
@@ -852,33 +859,56 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           }
       }
 
-      uint32_t pb[NT][NG][2];
+      uint32_t pb[NG][2];
 #pragma unroll
-      for (int s = 0; s < NT; ++s)
+      for (int g = 0; g < NG; ++g) {
+        float y[NT][2], top[NT];
+        bool past = false;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const float y[2] = {w[s][0] + lv[g][0], w[s][1] + lv[g][1]};
-          float top = fmaxf(y[0], y[1]);
-          if (__any_sync(0xffffffffu, top > m[s][g] + 15.f)) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float next = fmaxf(m[s][g], top - 7.f), f = ex2(m[s][g] - next);
-            m[s][g] = next;
-            l[s][g] *= f, zc[s][g] *= f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[s][g][j][i] *= f;
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p = ex2(y[i] - m[s][g]), hi = __half2float(__float2half_rn(p));
-            const __half2 both = __floats2half2_rn(p, (p - hi) * 2048.f);
-            pb[s][g][i] = movmatrix(*reinterpret_cast<const uint32_t*>(&both));
-            l[s][g] = fmaf(p, rv[g][i], l[s][g]);
-            if (C::kPar) zc[s][g] = fmaf(p, vz[g][i], zc[s][g]);
-          }
+        for (int s = 0; s < NT; ++s) {
+          y[s][0] = w[s][0] + lv[g][0], y[s][1] = w[s][1] + lv[g][1];
+          top[s] = fmaxf(y[s][0], y[s][1]);
+          past |= top[s] > m[s][g] + 15.f;
         }
+        if (__any_sync(0xffffffffu, past)) {
+          float f[NT];
+#pragma unroll
+          for (int s = 0; s < NT; ++s) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top[s] = fmaxf(top[s], __shfl_xor_sync(0xffffffffu, top[s], d));
+            const float next = fmaxf(m[s][g], top[s] - 7.f);
+            f[s] = ex2(m[s][g] - next);
+            m[s][g] = next;
+            l[s][g] *= f[s], zc[s][g] *= f[s];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[g][j][i] *= f[(i & 1) % NT];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          __half2 pair;
+          if (NT == 1) {
+            const float p = ex2(y[0][i] - m[0][g]), hi = __half2float(__float2half_rn(p));
+            pair = __floats2half2_rn(p, (p - hi) * 2048.f);
+            l[0][g] = fmaf(p, rv[g][i], l[0][g]);
+            if (C::kPar) zc[0][g] = fmaf(p, vz[g][i], zc[0][g]);
+          } else {
+            float p[NT];
+#pragma unroll
+            for (int s = 0; s < NT; ++s) p[s] = ex2(y[s][i] - m[s][g]);
+            pair = __floats2half2_rn(p[0], p[NT - 1]);
+            const float r[2] = {__low2float(pair), __high2float(pair)};
+#pragma unroll
+            for (int s = 0; s < NT; ++s) {
+              l[s][g] = fmaf(p[s] < 0x1p-14f ? p[s] : r[s], rv[g][i], l[s][g]);
+              if (C::kPar) zc[s][g] = fmaf(r[s], vz[g][i], zc[s][g]);
+            }
+          }
+          pb[g][i] = movmatrix(*reinterpret_cast<const uint32_t*>(&pair));
+        }
+      }
 
       // values: the lane's tokens 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, dimensions 16 g8 .. 16 g8 + 15
 #pragma unroll
@@ -895,11 +925,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const uint32_t y = half < 2 ? __byte_perm(v[2].x, v[3].x, sel) : __byte_perm(v[2].y, v[3].y, sel);
             const uint32_t x0 = low4(x), x2 = low4(x >> 8), y0 = low4(y), y2 = low4(y >> 8);
             const uint32_t x1 = high4(x), x3 = high4(x >> 8), y1 = high4(y), y3 = high4(y >> 8);
-#pragma unroll
-            for (int s = 0; s < NT; ++s) {
-              mma(o[s][g][2 * half], x0, x2, y0, y2, pb[s][g][0], pb[s][g][1]);
-              mma(o[s][g][2 * half + 1], x1, x3, y1, y3, pb[s][g][0], pb[s][g][1]);
-            }
+            mma(o[g][2 * half], x0, x2, y0, y2, pb[g][0], pb[g][1]);
+            mma(o[g][2 * half + 1], x1, x3, y1, y3, pb[g][0], pb[g][1]);
           }
         } else if (VB == 8) {
           uint4 v[4];
@@ -912,15 +939,13 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
             const uint32_t x = __byte_perm(v0[j >> 1], v1[j >> 1], sel), y = __byte_perm(v2[j >> 1], v3[j >> 1], sel);
             const uint32_t x0 = low8(x), x1 = low8(x >> 8), y0 = low8(y), y1 = low8(y >> 8);
-#pragma unroll
-            for (int s = 0; s < NT; ++s) mma(o[s][g][j], x0, x1, y0, y1, pb[s][g][0], pb[s][g][1]);
+            mma(o[g][j], x0, x1, y0, y1, pb[g][0], pb[g][1]);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint4 v = ldmatrix_x4_trans(vb ^ (32 * j));
-#pragma unroll
-            for (int s = 0; s < NT; ++s) mma(o[s][g][j], v.x, v.y, v.z, v.w, pb[s][g][0], pb[s][g][1]);
+            mma(o[g][j], v.x, v.y, v.z, v.w, pb[g][0], pb[g][1]);
           }
         }
       }
@@ -932,6 +957,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     float* dump = reinterpret_cast<float*>(ring_ptr + istage * C::kStage);
     if (lane == 0) dump_at[warp] = warp * S * C::kStage + istage * C::kStage;
     const int slot = seg.tile0 == 0;  // 0: the item began in an earlier share
+    // query(s, t4)'s sum from a lane's two columns
+    const auto column = [](float a, float b, int s) { return NT == 1 ? fmaf(b, 0x1p-11f, a) : s ? b : a; };
     if (seg.n != seg.nt && slot)
       record = make_int4(seg.b * a.q_heads + seg.hq0, seg.nq, (seg.from + seg.nt - 1) / plan.share, 0);
 #pragma unroll
@@ -946,13 +973,13 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         float* row = dump + t4 * kDumpRow;
 #pragma unroll
         for (int j = 0; j < 8; j += (VB == 16 ? 1 : 2)) {
-          const float(&e)[4] = o[s][g][j];
-          const float e0 = fmaf(e[1], 0x1p-11f, e[0]), e1 = fmaf(e[3], 0x1p-11f, e[2]);
+          const float(&e)[4] = o[g][j];
+          const float e0 = column(e[0], e[1], s), e1 = column(e[2], e[3], s);
           if (VB == 16) {
             row[20 * j + g8] = e0, row[20 * j + 8 + g8] = e1;
           } else {
-            const float(&f)[4] = o[s][g][(j + 1) & 7];
-            const float f0 = fmaf(f[1], 0x1p-11f, f[0]), f1 = fmaf(f[3], 0x1p-11f, f[2]), z = -zc[s][g];
+            const float(&f)[4] = o[g][(j + 1) & 7];
+            const float f0 = column(f[0], f[1], s), f1 = column(f[2], f[3], s), z = -zc[s][g];
             const float r0 = fmaf(e0, 512.f, z), r1 = fmaf(e1, 512.f, z), r2 = fmaf(f0, 512.f, z), r3 = fmaf(f1, 512.f, z);
             // 4 bits: rows (0, 2) and (1, 3) of four dimensions; 8 bits: (0, 1) and (2, 3)
             *reinterpret_cast<float4*>(row + 20 * g8 + 2 * j) =
@@ -963,13 +990,13 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         team_barrier();
         if (lt >= 2) {
           for (int j = tw; j < 4; j += T)
-            if (4 * s + j < seg.nq) {
+            if (query(s, j) < seg.nq) {
               float r[4], top, den;
               gather4(smem, dump_at + warp - tw, sml, T, j, lane, r, top, den);
               if (seg.n == seg.nt) {
-                store_out4(a, signs, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, lane, r, den);
+                store_out4(a, signs, seg.b * a.q_heads + seg.hq0 + query(s, j), D, g, lane, r, den);
               } else {
-                float* to = a.ws + (((int64_t)worker * 2 + slot) * a.qper + 4 * s + j) * (D + 4);
+                float* to = a.ws + (((int64_t)worker * 2 + slot) * a.qper + query(s, j)) * (D + 4);
                 __stcg(reinterpret_cast<float4*>(to + g * kGroup + 4 * lane), make_float4(r[0], r[1], r[2], r[3]));
                 if (lane == 0) __stcg(reinterpret_cast<float2*>(to + D + 2 * g), make_float2(top, den));
               }
@@ -994,7 +1021,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
               r[4 * c + 2] = fmaf(f, v.z, r[4 * c + 2]), r[4 * c + 3] = fmaf(f, v.w, r[4 * c + 3]);
             }
           }
-          store_out(a, signs, 4 * s + j < seg.nq, seg.b * a.q_heads + seg.hq0 + 4 * s + j, D, g, c8, r, den);
+          store_out(a, signs, query(s, j) < seg.nq, seg.b * a.q_heads + seg.hq0 + query(s, j), D, g, c8, r, den);
         }
         team_barrier();  // the stage, the statistics and the queries may be overwritten
       }
@@ -1112,14 +1139,10 @@ struct Split {
   int nqb, qper, may_cut;
 };
 
-// Queries a pass over the cache: eight, or four of 256 dimensions (a warp's sums are its registers'
-// bound; eight took 255 of them, with spills, and ran 35.0 us where two passes take 33.8, the second
-// mostly from L2).
-
-Split split_of(int page, int dim, int kv_heads, int q_heads, int max_pages) {
+Split split_of(int page, int kv_heads, int q_heads, int max_pages) {
   Split s;
-  const int group = q_heads / kv_heads, most = dim == kGroup ? kQ : kQ / 2;
-  s.nqb = (group + most - 1) / most;
+  const int group = q_heads / kv_heads;
+  s.nqb = (group + kQ - 1) / kQ;
   s.qper = (group + s.nqb - 1) / s.nqb;
   s.may_cut = (int64_t)max_pages * page > kWholeTiles * kTile;
   return s;
@@ -1135,7 +1158,7 @@ unsigned take_attn_error() {
 }
 
 size_t attn_workspace_bytes(const qlin_kv_desc* d, int q_heads, int, int max_pages) {
-  const Split s = split_of(d->page_size, d->head_dim, d->kv_heads, q_heads, max_pages);
+  const Split s = split_of(d->page_size, d->kv_heads, q_heads, max_pages);
   if (!s.may_cut) return 0;
   return kRecordBytes + (size_t)kMaxTeams * 2 * s.qper * (d->head_dim + 4) * sizeof(float);
 }
@@ -1143,7 +1166,7 @@ size_t attn_workspace_bytes(const qlin_kv_desc* d, int q_heads, int, int max_pag
 qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_stride, int q_heads,
                                const int32_t* block_table, int max_pages, const int32_t* seq_lens, int batch,
                                const uint32_t* sign_bits, float scale, __half* out, void* workspace, cudaStream_t s) {
-  const Split sp = split_of(c.page, c.dim, c.heads, q_heads, max_pages);
+  const Split sp = split_of(c.page, c.heads, q_heads, max_pages);
   AttnArgs a;
   a.c = c;
   a.q = q;
@@ -1166,8 +1189,8 @@ qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_strid
   a.nqb = sp.nqb;
   a.qper = sp.qper;
   a.may_cut = sp.may_cut;
-  if (c.dim != kGroup) return launch_widths<2, 1>(a, s);
-  return sp.qper > 4 ? launch_widths<1, 2>(a, s) : launch_widths<1, 1>(a, s);
+  if (sp.qper > 4) return c.dim == kGroup ? launch_widths<1, 2>(a, s) : launch_widths<2, 2>(a, s);
+  return c.dim == kGroup ? launch_widths<1, 1>(a, s) : launch_widths<2, 1>(a, s);
 }
 
 }  // namespace qlin

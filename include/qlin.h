@@ -440,8 +440,9 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  * softmax statistics and sums are fp32.  For 4- and 8-bit keys x enters the scores
  * as 16-bit integers with one power-of-two scale per group of 128 (exact for values
  * within a factor 8 of the group's largest, others rounded at 2^-14 of it, far
- * below half a step of the keys); the softmax weights enter the value sums with 22
- * bits.  An infinity or NaN among a head's query, keys or values within the length
+ * below half a step of the keys).  The softmax weights (times the values' scales)
+ * enter the value sums with 22 bits for up to four queries a kv head, above with 11,
+ * alike in numerator and denominator.  An infinity or NaN among a head's query, keys or values within the length
  * gives NaN there; what lies past the length has no effect.  Deterministic.
    q     : device fp16, sequence b's heads [q_heads][head_dim] at element offset
  *           b * q_stride; q_stride >= q_heads * head_dim, a multiple of 8;
