@@ -401,19 +401,13 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* sig
   f32x2 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = pair2(r[2 * i] * inv, r[2 * i + 1] * inv);
-  uint4 h0, h1;
-  if (a.sign_bits) {
-    uint32_t flip[8];
-    sign_masks(signs + 4 * g, t, flip);
-    fwht128_oct(v, t);
-    float_to_halves(v, h0, h1);
-    flip16(h0, h1, flip);
-  } else {
-    float_to_halves(v, h0, h1);
-  }
+  uint4 h[2];
+  if (a.sign_bits) fwht128<8>(v, t);
+  float_to_halves(v, h);
+  if (a.sign_bits) flip(h[0], sign_mask<8>(signs + 4 * g, t, 0)), flip(h[1], sign_mask<8>(signs + 4 * g, t, 1));
   if (!live) return;
   uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)row * dim + g * kGroup) + t;
-  out[0] = h0, out[8] = h1;
+  out[0] = h[0], out[8] = h[1];
 }
 
 // Prepares group g of a query (rotation, fp16, digits or halves) in its team's shared
@@ -425,21 +419,20 @@ __device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t*
                                               int t, uint8_t* sq, float2* sx) {
   constexpr int D = NG * kGroup;
   f32x2 p[8];
+  uint4 h[2] = {r0, r1};
   if (a.sign_bits) {
-    uint32_t flip[8];
-    sign_masks(signs + 4 * g, t, flip);
-    flip16(r0, r1, flip);
-    halves_to_float(r0, r1, p);
-    fwht128_oct(p, t);
-    float_to_halves(p, r0, r1);
+    flip(h[0], sign_mask<8>(signs + 4 * g, t, 0)), flip(h[1], sign_mask<8>(signs + 4 * g, t, 1));
+    halves_to_float(h, p);
+    fwht128<8>(p, t);
+    float_to_halves(p, h);
   }
   if (KB == 16) {
     uint4* dst = reinterpret_cast<uint4*>(sq + (q * D + g * kGroup) * 2) + t;
-    dst[0] = r0, dst[8] = r1;
+    dst[0] = h[0], dst[8] = h[1];
     if (t == 0) sx[q * NG + g] = make_float2(a.scale_log2e, 0.f);
     return;
   }
-  halves_to_float(r0, r1, p);
+  halves_to_float(h, p);
   float v[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) split2(p[i], v[2 * i], v[2 * i + 1]);

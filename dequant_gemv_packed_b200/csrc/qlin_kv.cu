@@ -14,16 +14,21 @@
 // Every step is one IEEE fp32 operation and the butterfly strides run 1, 2, ...,
 // 64, so the stored bytes are a function of the input alone.
 //
-// Eight lanes a group, 16 values each: strides 1, 2, 4 and 64 in the lane, 8 to 32
-// over lane distances 1, 2, 4; a warp has four groups of one side (K or V,
-// which may differ in width) and strides over the tokens with its lanes' signs kept.
+// Four lanes a group, 32 values each (eight and 16 while there are few groups):
+// strides 1, 2, 4, 32 and 64 in the lane, 8 and 16 over lane distances 1, 2; a warp
+// has eight groups of one side (K or V, which may differ in width) and strides over
+// the tokens, the next group's data and the slot after it in flight.
 // The quotients v / s share one correctly rounded reciprocal r and take three
 // multiply-adds each, q0 = v r, q0 + (v - q0 s) r: correctly rounded by Markstein's
 // theorem (IBM Journal of Research and Development 34, 1990), s having 11
 // significant bits and nothing here nearing the ends of the exponent range.
-// Bound by issue slots beside HBM: a rotated group costs 48 shuffles a warp of four,
-// so the rest is written in two-value operations (reading 30,001 rotated tokens of 8
-// heads took 574 instructions a warp and 84 us before, HBM's share being 26 us).
+// Bound by HBM's writes and by issue slots, which add up: reading 30,001 rotated
+// tokens of 8 heads at 4/8 bits takes 53.6 us; 31 with the rotation and the cache's
+// loads left out (a plain fill of the 123 MB it writes takes 32), 41 with the stores
+// left out.  With 574 instructions a warp of four groups it took 84; two-
+// value operations, constants in place of divisions and four lanes a group brought
+// it here.  Four lanes against eight: 16,384 unrotated wide tokens written and read
+// 41.1 us against 48.8, 16 tokens 6.3 against 5.6.
 #include "qlin_kv.cuh"
 #include "qlin_sm100.cuh"
 
@@ -33,9 +38,8 @@ namespace {
 __device__ unsigned int g_kv_error;
 
 constexpr int kThreads = 256;
-constexpr int kUnitsPerCta = kThreads / 16;  // groups of each side
-constexpr int kCtas = 4;  // an SM
-constexpr int kMaxGrid = 148 * kCtas;
+constexpr int units_per_cta(int lanes) { return kThreads / (2 * lanes); }  // groups of each side
+constexpr int ctas(int lanes) { return lanes == 8 ? 4 : 2; }                 // an SM
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
@@ -46,6 +50,15 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   float d;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
+}
+
+// Sign masks of every lane's values, in shared memory: [group][lane][piece].
+template <int L>
+__device__ __forceinline__ void fill_masks(uint4* masks, const uint32_t* sign_bits, int groups) {
+  constexpr int C = 16 / L;
+  for (int i = threadIdx.x; i < groups * L * C; i += kThreads)
+    masks[i] = sign_mask<L>(sign_bits + 4 * (i / (L * C)), i / C % L, i % C);
+  __syncthreads();
 }
 
 struct KvArgs {
@@ -60,6 +73,7 @@ struct KvArgs {
 
 // A lane's walk over the groups (units) of its side: unit = (token, head, group), the group of 128
 // within the head fixed.
+template <int L>
 struct Walk {
   int side, g, bits, t;
   int tok, r;         // token, and head * groups + group
@@ -71,8 +85,8 @@ struct Walk {
   __device__ __forceinline__ Walk(const KvArgs& a, int lane, int warp) {
     lg = a.c.dim == kGroup ? 0 : 1;
     unit = a.c.heads << lg;
-    const unsigned u = blockIdx.x * kUnitsPerCta + (warp >> 1) * 4 + (lane >> 3), step = gridDim.x * kUnitsPerCta;
-    t = lane & 7;
+    const unsigned u = blockIdx.x * units_per_cta(L) + (warp >> 1) * (32 / L) + lane / L, step = gridDim.x * units_per_cta(L);
+    t = lane % L;
     side = warp & 1;
     bits = side ? a.c.v_bits : a.c.k_bits;
     tok = (int)(u / (unsigned)unit);
@@ -112,56 +126,62 @@ __device__ __forceinline__ int checked_slot(const KvArgs& a, int s, int t) {
 
 // The loops below keep the next unit's data and the slot of the one after it in flight.
 
-__global__ void __launch_bounds__(kThreads, kCtas) kv_write_kernel(const __grid_constant__ KvArgs a) {
+template <int L>
+__global__ void __launch_bounds__(kThreads, ctas(L)) kv_write_kernel(const __grid_constant__ KvArgs a) {
+  constexpr int C = 16 / L;  // pieces of eight values a lane
   grid_launch_dependents();
   grid_dependency_wait();
+  __shared__ uint4 masks[2 * L * C];
+  if (a.sign_bits) fill_masks<L>(masks, a.sign_bits, a.c.dim / kGroup);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Walk w(a, lane, warp);
+  Walk<L> w(a, lane, warp);
   const int64_t stride = w.side ? a.v_stride : a.k_stride;
   const uint4* src = reinterpret_cast<const uint4*>((w.side ? a.v_in : a.k_in) + w.g * kGroup) + w.t;
-  uint32_t flip[8];
-  if (a.sign_bits) sign_masks(a.sign_bits + 4 * w.g, w.t, flip);
-  uint4 n0, n1;
+  const uint4* mask = masks + (w.g * L + w.t) * C;
+  uint4 next[C];
   auto load = [&]() {
-    const int64_t at = (int64_t)min(w.tok, a.tokens - 1) * stride + (int64_t)w.head() * a.c.dim;
-    n0 = src[at >> 3], n1 = src[(at >> 3) + 8];
+    const uint4* in = src + (((int64_t)min(w.tok, a.tokens - 1) * stride + (int64_t)w.head() * a.c.dim) >> 3);
+#pragma unroll
+    for (int c = 0; c < C; ++c) next[c] = in[L * c];
   };
   int next_slot = slot_of(a, w.tok);
   load();
   while (__any_sync(0xffffffffu, w.tok < a.tokens)) {
     const int slot = checked_slot(a, next_slot, w.t);
-    uint4 r0 = n0, r1 = n1;
+    uint4 r[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) r[c] = next[c];
     uint8_t *row, *par;
     w.place(a, max(slot, 0), row, par);
     w.next();
     next_slot = slot_of(a, w.tok);
     load();
-    f32x2 v[8];
+    f32x2 v[4 * C];
     if (a.sign_bits) {
-      flip16(r0, r1, flip);
-      halves_to_float(r0, r1, v);
-      fwht128_oct(v, w.t);
-      if (w.bits == 16) float_to_halves(v, r0, r1);
+#pragma unroll
+      for (int c = 0; c < C; ++c) flip(r[c], mask[c]);
+      halves_to_float(r, v);
+      fwht128<L>(v, w.t);
+      if (w.bits == 16) float_to_halves(v, r);
     } else {
-      halves_to_float(r0, r1, v);
+      halves_to_float(r, v);
     }
     if (w.bits == 16) {
-      if (slot >= 0) {
-        reinterpret_cast<uint4*>(row)[w.t] = r0;
-        reinterpret_cast<uint4*>(row)[w.t + 8] = r1;
-      }
+      if (slot >= 0)
+#pragma unroll
+        for (int c = 0; c < C; ++c) reinterpret_cast<uint4*>(row)[w.t + L * c] = r[c];
       continue;
     }
     float lo = 0.f, hi = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4 * C; ++j) {
       float x, y;
       split2(v[j], x, y);
       lo = min_nan(lo, min_nan(x, y));
       hi = max_nan(hi, max_nan(x, y));
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
+    for (int o = 1; o < L; o <<= 1) {
       lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
@@ -178,40 +198,39 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_write_kernel(const __grid_
     // v / s + z lies within 1/16 of [0, qmax] unless the scale was cut or the group is not finite
     const bool clamp = !(span <= 65504.f);
     const f32x2 s2 = pair2(-s, -s), inv2 = pair2(inv, inv), z2 = pair2(z, z), round2 = pair2(8388608.f, 8388608.f);
-    uint32_t q[16];  // the code in the low byte: adding 2^23 rounds to an integer, ties to even
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const f32x2 q0 = mul2(v[j], inv2);
-      f32x2 y = add2(fma2(fma2(q0, s2, v[j]), inv2, q0), z2);
-      float y0, y1;
-      if (clamp) {
-        split2(y, y0, y1);
-        y = pair2(fminf(fmaxf(y0, 0.f), qmax), fminf(fmaxf(y1, 0.f), qmax));
+    for (int c = 0; c < C; ++c) {
+      uint32_t q[8];  // the code in the low byte: adding 2^23 rounds to an integer, ties to even
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 x = v[4 * c + i], q0 = mul2(x, inv2);
+        f32x2 y = add2(fma2(fma2(q0, s2, x), inv2, q0), z2);
+        float y0, y1;
+        if (clamp) {
+          split2(y, y0, y1);
+          y = pair2(fminf(fmaxf(y0, 0.f), qmax), fminf(fmaxf(y1, 0.f), qmax));
+        }
+        split2(add2(y, round2), y0, y1);
+        q[2 * i] = __float_as_uint(y0);
+        q[2 * i + 1] = __float_as_uint(y1);
       }
-      split2(add2(y, round2), y0, y1);
-      q[2 * j] = __float_as_uint(y0);
-      q[2 * j + 1] = __float_as_uint(y1);
-    }
-    if (slot < 0) continue;
-    if (w.bits == 8) {
-      uint32_t c[4];
+      if (slot < 0) continue;
+      if (w.bits == 8) {
+        uint32_t b[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040),
-                           0x5410);
-      reinterpret_cast<uint2*>(row)[w.t] = make_uint2(c[0], c[1]);
-      reinterpret_cast<uint2*>(row)[w.t + 8] = make_uint2(c[2], c[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i)
+          b[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040),
+                             0x5410);
+        reinterpret_cast<uint2*>(row)[w.t + L * c] = make_uint2(b[0], b[1]);
+      } else {
         uint32_t b[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) b[k] = q[8 * i + 2 * k] + (q[8 * i + 2 * k + 1] << 4);
-        reinterpret_cast<uint32_t*>(row)[w.t + 8 * i] =
+        for (int k = 0; k < 4; ++k) b[k] = q[2 * k] + (q[2 * k + 1] << 4);
+        reinterpret_cast<uint32_t*>(row)[w.t + L * c] =
             __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
       }
     }
-    if (w.t == 0) *reinterpret_cast<__half2*>(par) = __halves2half2(s16, z16);
+    if (w.t == 0 && slot >= 0) *reinterpret_cast<__half2*>(par) = __halves2half2(s16, z16);
   }
 }
 
@@ -222,42 +241,50 @@ __device__ __forceinline__ f32x2 dequant2(uint32_t a, uint32_t b, f32x2 inv_unit
   return mul2(s, fma2(x, inv_unit, z));
 }
 
-__global__ void __launch_bounds__(kThreads, kCtas) kv_read_kernel(const __grid_constant__ KvArgs a) {
+template <int L>
+__global__ void __launch_bounds__(kThreads, ctas(L)) kv_read_kernel(const __grid_constant__ KvArgs a) {
+  constexpr int C = 16 / L;  // pieces of eight values a lane
   grid_launch_dependents();
   grid_dependency_wait();
+  __shared__ uint4 masks[2 * L * C];
+  if (a.sign_bits) fill_masks<L>(masks, a.sign_bits, a.c.dim / kGroup);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Walk w(a, lane, warp);
+  Walk<L> w(a, lane, warp);
   const int64_t stride = (int64_t)a.c.heads * a.c.dim;
   uint4* dst = reinterpret_cast<uint4*>((w.side ? a.v_out : a.k_out) + w.g * kGroup) + w.t;
-  uint32_t flip[8];
-  if (a.sign_bits) sign_masks(a.sign_bits + 4 * w.g, w.t, flip);
-  uint4 n0 = make_uint4(0u, 0u, 0u, 0u), n1 = n0;
+  const uint4* mask = masks + (w.g * L + w.t) * C;
+  uint4 next[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) next[c] = make_uint4(0u, 0u, 0u, 0u);
   uint32_t next_par = 0;
   auto load = [&](int slot) {
     uint8_t *row, *par;
     w.place(a, max(slot, 0), row, par);
     if (w.bits == 16) {
-      n0 = reinterpret_cast<const uint4*>(row)[w.t];
-      n1 = reinterpret_cast<const uint4*>(row)[w.t + 8];
+#pragma unroll
+      for (int c = 0; c < C; ++c) next[c] = reinterpret_cast<const uint4*>(row)[w.t + L * c];
     } else {
       next_par = *reinterpret_cast<const uint32_t*>(par);
-      if (w.bits == 8) {
-        const uint2 c = reinterpret_cast<const uint2*>(row)[w.t], d = reinterpret_cast<const uint2*>(row)[w.t + 8];
-        n0 = make_uint4(c.x, c.y, d.x, d.y);
-      } else {
-        n0.x = reinterpret_cast<const uint32_t*>(row)[w.t];
-        n0.y = reinterpret_cast<const uint32_t*>(row)[w.t + 8];
-      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (w.bits == 8) {
+          const uint2 x = reinterpret_cast<const uint2*>(row)[w.t + L * c];
+          next[c].x = x.x, next[c].y = x.y;
+        } else {
+          next[c].x = reinterpret_cast<const uint32_t*>(row)[w.t + L * c];
+        }
     }
   };
   int next_slot = checked_slot(a, slot_of(a, w.tok), w.t);
   load(next_slot);
-  int tok = w.tok, head = w.head();  // of the unit in n0, n1
+  int tok = w.tok, head = w.head();  // of the unit in `next`
   w.next();
   int after = slot_of(a, w.tok);
   while (__any_sync(0xffffffffu, tok < a.tokens)) {
     const int slot = next_slot;
-    uint4 r0 = n0, r1 = n1;
+    uint4 r[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) r[c] = next[c];
     const uint32_t pp = next_par;
     uint4* out = dst + (((int64_t)tok * stride + (int64_t)head * a.c.dim) >> 3);
     const bool live = tok < a.tokens;
@@ -266,41 +293,44 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_read_kernel(const __grid_c
     tok = w.tok, head = w.head();
     w.next();
     after = slot_of(a, w.tok);
-    f32x2 v[8];
+    f32x2 v[4 * C];
     if (w.bits == 16) {
-      if (a.sign_bits) halves_to_float(r0, r1, v);
+      if (a.sign_bits) halves_to_float(r, v);
     } else {
       const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&pp));
       const f32x2 s = pair2(p.x, p.x), z = pair2(-p.y, -p.y);
-      const uint32_t x[4] = {r0.x, r0.y, r0.z, r0.w};
       if (w.bits == 8) {
         const f32x2 one = pair2(1.f, 1.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < C; ++c) {
+          const uint32_t x[2] = {r[c].x, r[c].y};
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            v[2 * i + k] = dequant2(__byte_perm(x[i], 0x4B000000u, 0x7440 + 2 * k),
-                                    __byte_perm(x[i], 0x4B000000u, 0x7441 + 2 * k), one, z, s);
+          for (int i = 0; i < 4; ++i)
+            v[4 * c + i] = dequant2(__byte_perm(x[i >> 1], 0x4B000000u, 0x7440 + 2 * (i & 1)),
+                                    __byte_perm(x[i >> 1], 0x4B000000u, 0x7441 + 2 * (i & 1)), one, z, s);
+        }
       } else {
         const f32x2 u0 = pair2(1.f, 0.0625f), u2 = pair2(0x1p-8f, 0x1p-12f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t y = x[i] >> (16 * k);
-            v[4 * i + 2 * k] = dequant2((y & 0xFu) | 0x4B000000u, (y & 0xF0u) | 0x4B000000u, u0, z, s);
-            v[4 * i + 2 * k + 1] = dequant2((y & 0xF00u) | 0x4B000000u, (y & 0xF000u) | 0x4B000000u, u2, z, s);
+            const uint32_t y = r[c].x >> (16 * k);
+            v[4 * c + 2 * k] = dequant2((y & 0xFu) | 0x4B000000u, (y & 0xF0u) | 0x4B000000u, u0, z, s);
+            v[4 * c + 2 * k + 1] = dequant2((y & 0xF00u) | 0x4B000000u, (y & 0xF000u) | 0x4B000000u, u2, z, s);
           }
       }
     }
-    if (a.sign_bits) fwht128_oct(v, w.t);
-    if (a.sign_bits || w.bits != 16) float_to_halves(v, r0, r1);
-    if (a.sign_bits) flip16(r0, r1, flip);
-    if (slot < 0) r0 = r1 = make_uint4(0u, 0u, 0u, 0u);
-    if (live) {
-      out[0] = r0;
-      out[8] = r1;
+    if (a.sign_bits) fwht128<L>(v, w.t);
+    if (a.sign_bits || w.bits != 16) float_to_halves(v, r);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (a.sign_bits) flip(r[c], mask[c]);
+      if (slot < 0) r[c] = make_uint4(0u, 0u, 0u, 0u);
     }
+    if (live)
+#pragma unroll
+      for (int c = 0; c < C; ++c) out[L * c] = r[c];
   }
 }
 
@@ -313,31 +343,37 @@ unsigned take_kv_error() {
   return v;
 }
 
-// Units and a step beyond them are counted in 31 bits.
-static qlin_status kv_grid(const KvArgs& a, unsigned* grid) {
+// Four lanes a group once every CTA has two rounds of them, else eight.
+static int lanes_for(int64_t units) { return units >= 2 * 148 * ctas(4) * units_per_cta(4) ? 4 : 8; }
+
+// Blocks for the units (a token's groups of one side), counted with a step beyond them in 31 bits.
+static qlin_status kv_grid(const KvArgs& a, int& lanes, unsigned& grid) {
   const int64_t units = (int64_t)a.tokens * a.c.heads * (a.c.dim / kGroup);
-  if (units > 0x7fffffffLL - 2 * kMaxGrid * kUnitsPerCta) return QLIN_ERR_SHAPE;
-  const int64_t need = (units + kUnitsPerCta - 1) / kUnitsPerCta;
-  *grid = (unsigned)(need < kMaxGrid ? need : kMaxGrid);
+  if (units > 0x7fffffffLL - (1 << 20)) return QLIN_ERR_SHAPE;
+  lanes = lanes_for(units);
+  const int64_t need = (units + units_per_cta(lanes) - 1) / units_per_cta(lanes), most = 148 * ctas(lanes);
+  grid = (unsigned)(need < most ? need : most);
   return QLIN_OK;
 }
 
 qlin_status launch_kv_write(const KvView& c, const __half* k, const __half* v, int64_t k_stride, int64_t v_stride,
                             const int32_t* slots, int tokens, const uint32_t* sign_bits, cudaStream_t s) {
   const KvArgs a = {c, k, v, nullptr, nullptr, k_stride, v_stride, slots, sign_bits, tokens};
+  int lanes;
   unsigned grid;
-  const qlin_status r = kv_grid(a, &grid);
+  const qlin_status r = kv_grid(a, lanes, grid);
   if (r != QLIN_OK) return r;
-  return launch_dependent(kv_write_kernel, grid, kThreads, 0, s, a);
+  return launch_dependent(lanes == 4 ? kv_write_kernel<4> : kv_write_kernel<8>, grid, kThreads, 0, s, a);
 }
 
 qlin_status launch_kv_read(const KvView& c, __half* k, __half* v, const int32_t* slots, int tokens,
                            const uint32_t* sign_bits, cudaStream_t s) {
   const KvArgs a = {c, nullptr, nullptr, k, v, 0, 0, slots, sign_bits, tokens};
+  int lanes;
   unsigned grid;
-  const qlin_status r = kv_grid(a, &grid);
+  const qlin_status r = kv_grid(a, lanes, grid);
   if (r != QLIN_OK) return r;
-  return launch_dependent(kv_read_kernel, grid, kThreads, 0, s, a);
+  return launch_dependent(lanes == 4 ? kv_read_kernel<4> : kv_read_kernel<8>, grid, kThreads, 0, s, a);
 }
 
 }  // namespace qlin

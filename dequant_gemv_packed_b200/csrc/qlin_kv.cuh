@@ -78,8 +78,9 @@ __device__ __forceinline__ int div_pos(int n, int d) {
   return q + (rest >= d);
 }
 
-// A group of 128 values on eight lanes: lane t = lane % 8 has values 8 t .. 8 t + 7 (v[0..7]) and
-// 64 + 8 t .. 64 + 8 t + 7 (v[8..15]), so that 16-byte pieces of halves are contiguous over the lanes.
+// A group of 128 values on L = 8 or 4 lanes: lane t = lane % L has the values 8 L c + 8 t ..
+// 8 L c + 8 t + 7, c = 0 .. 16 / L - 1, as pairs v[4 c + i], so that 16-byte pieces of halves are
+// contiguous over the lanes.
 
 // Two fp32 values in one register pair; each operation rounds both to nearest, like two single ones.
 using f32x2 = unsigned long long;
@@ -107,13 +108,15 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return d;
 }
 
-// Butterflies of strides 1..64 (1, 2, 4 in the lane, 8, 16, 32 across lanes, 64 in the lane), then
-// the scaling.  A difference a - b is the multiply-add b (-1) + a, and across lanes both halves are
+// Butterflies of strides 1..64 (1, 2, 4 in the lane, then across the L lanes, then over c), then the
+// scaling.  A difference a - b is the multiply-add b (-1) + a, and across lanes both halves are
 // v (+-1) + p: one rounding each, as the definition has it.
-__device__ __forceinline__ void fwht128_oct(f32x2 (&p)[8], int t) {
+template <int L>
+__device__ __forceinline__ void fwht128(f32x2 (&p)[64 / L], int t) {
+  constexpr int N = 64 / L;
   const f32x2 minus = pair2(-1.f, -1.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < N; ++j) {
     float a, b;
     split2(p[j], a, b);
     p[j] = pair2(__fadd_rn(a, b), __fsub_rn(a, b));
@@ -121,67 +124,77 @@ __device__ __forceinline__ void fwht128_oct(f32x2 (&p)[8], int t) {
 #pragma unroll
   for (int h = 1; h < 4; h <<= 1)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < N; ++j)
       if (!(j & h)) {
         const f32x2 a = p[j], b = p[j + h];
         p[j] = add2(a, b);
         p[j + h] = fma2(b, minus, a);
       }
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
+  for (int o = 1; o < L; o <<= 1) {
     const float sign = (t & o) ? -1.f : 1.f;
     const f32x2 s = pair2(sign, sign);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < N; ++j) {
       float lo, hi;
       split2(p[j], lo, hi);
       p[j] = fma2(p[j], s, pair2(__shfl_xor_sync(0xffffffffu, lo, o), __shfl_xor_sync(0xffffffffu, hi, o)));
     }
   }
+#pragma unroll
+  for (int h = 4; h < N; h <<= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (!(j & h)) {
+        const f32x2 a = p[j], b = p[j + h];
+        p[j] = add2(a, b);
+        p[j + h] = fma2(b, minus, a);
+      }
   const f32x2 scale = pair2(kInvSqrt128, kInvSqrt128);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const f32x2 a = p[j], b = p[j + 4];
-    p[j] = mul2(add2(a, b), scale);
-    p[j + 4] = mul2(fma2(b, minus, a), scale);
+  for (int j = 0; j < N; ++j) p[j] = mul2(p[j], scale);
+}
+
+// Sign masks of the lane's piece c as four pairs of halves; `words` are the group's four.
+template <int L>
+__device__ __forceinline__ uint4 sign_mask(const uint32_t* words, int t, int c) {
+  const int at = 8 * L * c + 8 * t;
+  const uint32_t sw = words[at >> 5] >> (at & 31);
+  uint32_t m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = ((sw >> (2 * i)) & 1u) << 15 | ((sw >> (2 * i + 1)) & 1u) << 31;
+  return make_uint4(m[0], m[1], m[2], m[3]);
+}
+
+__device__ __forceinline__ void flip(uint4& r, const uint4& m) { r.x ^= m.x, r.y ^= m.y, r.z ^= m.z, r.w ^= m.w; }
+
+template <int C>
+__device__ __forceinline__ void halves_to_float(const uint4 (&r)[C], f32x2 (&v)[4 * C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t w[4] = {r[c].x, r[c].y, r[c].z, r[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[4 * c + i] = pair2(f.x, f.y);
+    }
   }
 }
 
-// Sign masks of the lane's 16 values, as eight pairs of halves; `words` are the group's four.
-__device__ __forceinline__ void sign_masks(const uint32_t* words, int t, uint32_t (&m)[8]) {
+template <int C>
+__device__ __forceinline__ void float_to_halves(const f32x2 (&v)[4 * C], uint4 (&r)[C]) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t sw = words[2 * k + (t >> 2)] >> (8 * (t & 3));
+  for (int c = 0; c < C; ++c) {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[4 * k + i] = ((sw >> (2 * i)) & 1u) << 15 | ((sw >> (2 * i + 1)) & 1u) << 31;
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      split2(v[4 * c + i], a, b);
+      const __half2 h = __floats2half2_rn(a, b);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    r[c] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-
-__device__ __forceinline__ void flip16(uint4& r0, uint4& r1, const uint32_t (&m)[8]) {
-  r0.x ^= m[0], r0.y ^= m[1], r0.z ^= m[2], r0.w ^= m[3];
-  r1.x ^= m[4], r1.y ^= m[5], r1.z ^= m[6], r1.w ^= m[7];
-}
-
-__device__ __forceinline__ void halves_to_float(const uint4& r0, const uint4& r1, f32x2 (&v)[8]) {
-  const uint32_t raw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[i]));
-    v[i] = pair2(f.x, f.y);
-  }
-}
-
-__device__ __forceinline__ void float_to_halves(const f32x2 (&v)[8], uint4& r0, uint4& r1) {
-  uint32_t raw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float a, b;
-    split2(v[i], a, b);
-    const __half2 h = __floats2half2_rn(a, b);
-    raw[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  r0 = make_uint4(raw[0], raw[1], raw[2], raw[3]);
-  r1 = make_uint4(raw[4], raw[5], raw[6], raw[7]);
 }
 
 }  // namespace qlin

@@ -587,6 +587,32 @@ def test_write_and_read_many_tokens():
             assert np.array_equal(g.cpu().numpy(), r)
 
 
+@pytest.mark.parametrize("dim,rotate", [(128, True), (256, False)])
+@pytest.mark.parametrize("kb,vb", WIDTHS)
+def test_write_and_read_a_prompt(kb, vb, dim, rotate):
+    """So many groups (from 18,944 a side) that the kernels take four lanes a group."""
+    rng = np.random.default_rng(kb + 3 * vb + dim)
+    heads = 8 if dim == 128 else 5
+    t = 2400 if dim == 128 else 1911
+    c = D.Cache(t // 32 + 2, 32, heads, dim, kb, vb)
+    slots = rng.permutation(c.bytes.shape[0] * 32)[:t].astype(np.int32)
+    slots[5::89] = -2
+    sb = signs(rng, dim, rotate)
+    k, v = vectors(rng, t, heads, dim), vectors(rng, t, heads, dim)
+    k[7, 0, 3], v[8, 1, 5], k[9] = np.nan, -np.inf, 0
+    d, pool = kv_desc(c), pool_of(c)
+    Q.qlin_kv_write(d, pool, dev(k), dev(v), dev(slots), sign_bits=dev(sb))
+    c.write(k, v, slots, sb)
+    got, ref = pool.cpu().numpy().reshape(c.bytes.shape), c.bytes
+    if kb == 16:  # a NaN's payload is not part of the format
+        got, ref = got.view(np.float16), ref.view(np.float16)
+        assert np.array_equal(got, ref, equal_nan=True)
+    else:
+        assert np.array_equal(got, ref)
+    for g, r in zip(Q.qlin_kv_read(d, pool, dev(slots), sign_bits=dev(sb)), c.read(slots, sb)):
+        assert np.array_equal(g.cpu().numpy(), r, equal_nan=True)
+
+
 # ----------------------------------------------------------------------- norm
 
 def check_norm(x, w, eps, res=None, **kw):
