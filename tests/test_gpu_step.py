@@ -498,6 +498,94 @@ def test_workspace_contents_do_not_matter():
         run_attention(c, q, table, lens, sb=sb, pool=pool, workspace=ws[:size - 16])
 
 
+def test_captured_behind_copies_memsets_and_joins():
+    """The calls wait for whatever precedes them: a host copy, a memset, and another stream's work
+    that is joined, eagerly and in a graph; and what follows them waits for them."""
+    c, q, table, lens, sb = long_case(36, (700, 90))
+    d, pool = kv_desc(c), pool_of(c)
+    tt, ts = dev(table.astype(np.int32)), dev(sb)
+    host_n, tl = torch.tensor(lens, dtype=torch.int32).pin_memory(), torch.zeros(2, dtype=torch.int32, device=DEV)
+    src, tq = dev(q), torch.zeros(2, 8, 128, dtype=torch.float16, device=DEV)
+    w = torch.ones(1024, dtype=torch.float16, device=DEV)
+    acc = torch.zeros(2, 1024, dtype=torch.float16, device=DEV)
+    other = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            big = src.float().repeat(400, 1, 1)  # work that takes a while
+            tq.copy_(big[:2])
+        tl.copy_(host_n, non_blocking=True)
+        here.wait_stream(other)
+        o = Q.qlin_attn_decode(d, pool, tq, tt, tl, sign_bits=ts)
+        acc.zero_()
+        y, r = Q.qlin_rmsnorm(o.flatten(1), w, 1e-6, residual=acc)
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            z = r.clone()
+        here.wait_stream(other)
+        tq.zero_()
+        tl.zero_()
+        return o, y, z
+
+    torch.cuda.synchronize()
+    ref = [x.clone() for x in step()]
+    torch.cuda.synchronize()
+    check_attention(ref[0], c, q, table, lens, sb=sb)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(step(), ref))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step()
+    for _ in range(20):
+        for x in outs:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+
+
+@pytest.mark.parametrize("overlap", [False, True])
+def test_beside_overlapping_layers(overlap):
+    """norm -> GEMV -> norm -> GEMV -> attention -> GEMV chains with and without the GEMVs' overlap give
+    the same bits, in a graph too."""
+    rng = np.random.default_rng(37)
+    c = filled(rng, 40, 16, 2, 128, 8, 8, None)
+    d, pool = kv_desc(c), pool_of(c)
+    table, n = dev(np.arange(40, dtype=np.int32).reshape(1, 40)), dev(np.array([630], np.int32))
+    la, lb = linear(1024, 512, 4, 3), linear(512, 1024, 6, 4)
+    x = dev(rng.standard_normal((1, 512)).astype(np.float16))
+    w = dev((1 + 0.1 * rng.standard_normal(512)).astype(np.float16))
+
+    def chain():
+        h, r = x, x
+        for _ in range(3):
+            h, r = Q.qlin_rmsnorm(h, w, 1e-6, residual=r)
+            q = Q.qlin_gemv(la[0], la[1], la[2].scales, la[2].zeros, la[3], h)
+            o = Q.qlin_attn_decode(d, pool, q.view(1, 8, 128), table, n)
+            h = Q.qlin_gemv(lb[0], lb[1], lb[2].scales, lb[2].zeros, lb[3], o.view(1, 1024))
+        return h, r
+
+    ref = [t.clone() for t in chain()]
+    torch.cuda.synchronize()
+    before = Q.qlin_set_overlap(overlap)
+    try:
+        for _ in range(30):
+            assert all(torch.equal(a, b) for a, b in zip(chain(), ref))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = chain()
+        for _ in range(10):
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+    finally:
+        Q.qlin_set_overlap(before)
+
+
 def test_first_call_inside_a_capture():
     """A process whose first calls are captured: nothing is set up outside the graph."""
     import os
