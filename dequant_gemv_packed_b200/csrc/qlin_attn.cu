@@ -86,6 +86,11 @@ __device__ __forceinline__ int item_extra(int lt) { return 4 + (4 << lt); }
 // write (16 dimensions of a query each) and those that read over the banks.
 constexpr int kDumpRow = 8 * 20 + 8;  // of a query
 constexpr int kMaxTeams = 3 * kSms;  // teams when items are cut: one a CTA
+// Up to here records are of items and not of teams, which spares the join its empty blocks: 28 items
+// cut among 148 teams take 31.0 us and not 31.3, 8 take 16.0 and not 17.3.  128 items take 23.3 by
+// team, 23.9 by item: a team begins at most one cut item, so there are blocks without work either way.
+constexpr int kItemRecords = 64;
+static_assert(kItemRecords <= kMaxTeams);
 constexpr int kRecordBytes = kMaxTeams * 16;  // of the workspace: the item that each team is the first to cut
 
 template <int KB, int VB, int NG, int NT>
@@ -124,12 +129,15 @@ struct AttnArgs {
   const int32_t *table, *lens;
   const uint32_t* sign_bits;
   __half* out;
-  int4* records;  // [teams] (first output row, queries, last team, -) of the item that a team begins and cuts; 0 queries: none
+  // (first output row, queries, first team, last team) of cut items, 0 queries: none: of every item if
+  // there are at most kItemRecords, else of the item that each team begins and cuts
+  int4* records;
   float* ws;  // [teams][2] slots of [qper][dim + 4]: sums, then maximum and denominator per group
   float scale_log2e;
   int32_t q_heads, max_pages, batch, cap;  // cap: tokens the table can hold
   int32_t group, items, nqb, qper;  // queries a kv head;             // (head, query block) pairs of a sequence; blocks; queries a block
   int32_t page_shift;                      // log2 of a page's tiles; -1: no power of two
+  int32_t by_item;                         // records are of items
   int32_t may_cut;                         // the table has room for more than kWholeTiles tiles
 };
 
@@ -317,6 +325,7 @@ struct Segment {
   int b, hq0, nq, h;  // sequence, first query head and how many, kv head
   int tile0, n, nt;   // tiles [tile0, tile0 + n) of nt
   int len, from;      // tokens of the sequence; position of the item's first tile
+  int item;           // in all
 };
 
 // A team's place in its share: position, sequence, the sequence's first position and tiles.
@@ -342,6 +351,7 @@ __device__ __forceinline__ bool next_segment(const AttnArgs& a, const Plan& p, c
     s.nq = min(a.qper, a.group - q0);
     s.hq0 = s.h * a.group + q0;
     s.from = first + item * cost + p.extra;
+    s.item = b * a.items + item;
     cur = make_int4(u, b, first, nt);
     return true;
   }
@@ -952,8 +962,12 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     const int slot = seg.tile0 == 0;  // 0: the item began in an earlier share
     // query(s, t4)'s sum from a lane's two columns
     const auto column = [](float a, float b, int s) { return NT == 1 ? fmaf(b, 0x1p-11f, a) : s ? b : a; };
-    if (seg.n != seg.nt && slot)
-      record = make_int4(seg.b * a.q_heads + seg.hq0, seg.nq, (seg.from + seg.nt - 1) / plan.share, 0);
+    if (a.may_cut && slot) {
+      int4 rec = make_int4(0, 0, 0, 0);
+      if (seg.n != seg.nt)
+        record = rec = make_int4(seg.b * a.q_heads + seg.hq0, seg.nq, worker, (seg.from + seg.nt - 1) / plan.share);
+      if (a.by_item && tw == 0 && lane == 0) a.records[seg.item] = rec;
+    }
 #pragma unroll
     for (int s = 0; s < NT; ++s)
 #pragma unroll
@@ -1032,47 +1046,50 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   for (int b = blockIdx.x; b < a.batch; b += grid) {
     const int n = a.lens[b];
     if (n > a.cap && threadIdx.x == 0) atomicOr(&g_attn_error, kKvBadLength);
-    if (n <= 0)
+    if (n <= 0) {
       for (int i = threadIdx.x; i < a.q_heads * D / 8; i += NW * 32)
         reinterpret_cast<uint4*>(a.out + (int64_t)b * a.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.may_cut && a.by_item && threadIdx.x < a.items) a.records[b * a.items + threadIdx.x] = make_int4(0, 0, 0, 0);
+    }
   }
 
-  if (a.may_cut && threadIdx.x == 0) a.records[blockIdx.x] = record;  // items are cut: a team is the CTA
+  if (a.may_cut && !a.by_item && threadIdx.x == 0) a.records[blockIdx.x] = record;  // a team that cuts is the CTA
 }
 
-// Joins the pieces of the item that team blockIdx.x begins and cuts, if there is one; a query
-// (blockIdx.y) a block, kJoinWarps warps over its pieces.
-constexpr int kJoinWarps = 8;
-
-template <int NG>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+// Joins the pieces of query blockIdx.y of the cut item of record blockIdx.x, W warps over the pieces.
+// What it costs is latency (3 to 4 us of a call that cuts, its launch among them): a record, its
+// pieces, the sums of the warps, and each stretch of code that runs for the first time.  So the code
+// is short: a piece or two a warp at a time and not four, 1.0 us less for one query head of 18 pieces.
+template <int NG, int W>
+__global__ void __launch_bounds__(W * 32) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int D = NG * kGroup;
-  __shared__ __align__(16) float sums[NG][kJoinWarps][kGroup];
-  __shared__ float2 sml[NG][kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = blockIdx.y, c0 = blockIdx.x;
+  constexpr int N = W == 4 ? 2 : 1;  // pieces that a warp loads at a time
+  __shared__ __align__(16) float sums[NG][W][kGroup];
+  __shared__ float2 sml[NG][W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = blockIdx.y;
   grid_launch_dependents();
   grid_dependency_wait();  // every block: this grid's end stands for the first one's too
-  const int4 rec = __ldcg(a.records + c0);
+  const int4 rec = __ldcg(a.records + blockIdx.x);
   if (q >= rec.y) return;
   float top[NG], den[NG], r[NG][4];
 #pragma unroll
   for (int g = 0; g < NG; ++g) top[g] = kNone, den[g] = r[g][0] = r[g][1] = r[g][2] = r[g][3] = 0.f;
-  for (int c = c0 + warp; c <= rec.z; c += 4 * kJoinWarps) {  // four pieces at a time
-    float4 v[4][NG];
-    float2 ml[4][NG];
+  for (int c = rec.z + warp; c <= rec.w; c += N * W) {
+    float4 v[N][NG];
+    float2 ml[N][NG];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = c + i * kJoinWarps;
-      const float* p = a.ws + (((int64_t)k * 2 + (k == c0)) * a.qper + q) * (D + 4);
+    for (int i = 0; i < N; ++i) {
+      const int k = c + i * W;
+      const float* p = a.ws + (((int64_t)k * 2 + (k == rec.z)) * a.qper + q) * (D + 4);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const bool live = k <= rec.z;
+        const bool live = k <= rec.w;
         ml[i][g] = live ? __ldcg(reinterpret_cast<const float2*>(p + D + 2 * g)) : make_float2(kNone, 0.f);
         v[i][g] = live ? __ldcg(reinterpret_cast<const float4*>(p + g * kGroup + 4 * lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const float next = fmaxf(top[g], ml[i][g].x), f = ex2(top[g] - next), e = ex2(ml[i][g].x - next);
@@ -1088,19 +1105,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     if (lane == 0) sml[g][warp] = make_float2(top[g], den[g]);
   }
   __syncthreads();
-  if (warp >= NG) return;
-  float t = kNone, d = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int g = warp; g < NG; g += W) {
+    float t = kNone, d = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) t = fmaxf(t, sml[warp][w].x);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float2 ml = sml[warp][w];
-    const float f = ex2(ml.x - t);
-    const float4 s = *reinterpret_cast<const float4*>(&sums[warp][w][4 * lane]);
-    d = fmaf(f, ml.y, d);
-    v[0] = fmaf(f, s.x, v[0]), v[1] = fmaf(f, s.y, v[1]), v[2] = fmaf(f, s.z, v[2]), v[3] = fmaf(f, s.w, v[3]);
+    for (int w = 0; w < W; ++w) t = fmaxf(t, sml[g][w].x);
+#pragma unroll 4
+    for (int w = 0; w < W; ++w) {
+      const float2 ml = sml[g][w];
+      const float f = ex2(ml.x - t);
+      const float4 s = *reinterpret_cast<const float4*>(&sums[g][w][4 * lane]);
+      d = fmaf(f, ml.y, d);
+      v[0] = fmaf(f, s.x, v[0]), v[1] = fmaf(f, s.y, v[1]), v[2] = fmaf(f, s.z, v[2]), v[3] = fmaf(f, s.w, v[3]);
+    }
+    store_out4(a, a.sign_bits, rec.x + q, D, g, lane, v, d);
   }
-  store_out4(a, a.sign_bits, rec.x + q, D, warp, lane, v, d);
 }
 
 template <int KB, int VB, int NG, int NT>
@@ -1118,7 +1136,12 @@ qlin_status launch(const AttnArgs& a, cudaStream_t s) {
   }
   const qlin_status r = launch_dependent(attn_kernel<KB, VB, NG, NT>, C::kGrid, C::kWarps * 32, C::kSmem, s, a);
   if (r != QLIN_OK || !a.may_cut) return r;
-  return launch_dependent(attn_join_kernel<NG>, dim3(C::kGrid - 1, a.qper), kJoinWarps * 32, 0, s, a);
+  // Few items have many pieces.  16 warps a block and not 8: 17.0 us and not 17.7 at 8 items of 18
+  // pieces; 4 and not 8: 14.3 us and not 15.0 at 64 items of 2 or 3.
+  const int64_t items = (int64_t)a.batch * a.items;
+  if (items <= 8) return launch_dependent(attn_join_kernel<NG, 16>, dim3(items, a.qper), 16 * 32, 0, s, a);
+  if (items <= 32) return launch_dependent(attn_join_kernel<NG, 8>, dim3(items, a.qper), 8 * 32, 0, s, a);
+  return launch_dependent(attn_join_kernel<NG, 4>, dim3(a.by_item ? items : C::kGrid - 1, a.qper), 4 * 32, 0, s, a);
 }
 
 template <int NG, int NT>
@@ -1182,6 +1205,7 @@ qlin_status launch_attn_decode(const KvView& c, const __half* q, int64_t q_strid
   a.nqb = sp.nqb;
   a.qper = sp.qper;
   a.may_cut = sp.may_cut;
+  a.by_item = (int64_t)batch * a.items <= kItemRecords;
   if (sp.qper > 4) return c.dim == kGroup ? launch_widths<1, 2>(a, s) : launch_widths<2, 2>(a, s);
   return c.dim == kGroup ? launch_widths<1, 1>(a, s) : launch_widths<2, 1>(a, s);
 }

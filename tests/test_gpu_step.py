@@ -483,6 +483,33 @@ def test_query_with_an_outlying_channel(kb):
     check_attention(run_attention(c, q, table, [128]), c, q, table, [128])
 
 
+@pytest.mark.parametrize("dim,group,kb,vb", [(128, 3, 8, 4), (256, 2, 4, 8), (128, 12, 8, 8)])
+def test_one_workspace_through_calls_of_every_size(dim, group, kb, vb):
+    """1 to 66 (head, query block) pairs, on both sides of each count at which pieces are joined another
+    way; cut and whole items and empty sequences by turns, in the same workspace, full of ones at first."""
+    rng = np.random.default_rng(dim + group)
+    c1, c2 = (filled(rng, 60, 32, h, dim, kb, vb, None) for h in (1, 2))
+    blocks = -(-group // 8)
+    ws = None
+    for c in (c2, c1):
+        pool = pool_of(c)
+        for items in (66, 65, 64, 33, 32, 9, 8, 2, 1):
+            B = items // (c.heads * blocks)
+            if B * c.heads * blocks != items:
+                continue
+            table = rng.integers(0, 60, (B, 60))
+            q = rng.standard_normal((B, c.heads * group, dim)).astype(np.float16)
+            if ws is None:
+                ws = torch.full((Q.qlin_attn_workspace_bytes(kv_desc(c), c.heads * group, B, 60),), 0xFF,
+                                dtype=torch.uint8, device=DEV)
+            for long in (1900, 40, 1000, 0):  # cut, whole, cut elsewhere, none
+                lens = rng.integers(0, 60, B)
+                lens[B // 2] = long
+                lens[B - 1 if B > 2 else 0] = long // 2 if B > 2 else long
+                got = run_attention(c, q, table, lens, pool=pool, workspace=ws)
+                check_attention(got, c, q, table, lens, what=f"{items} of {long}")
+
+
 def test_workspace_contents_do_not_matter():
     c, q, table, lens, sb = long_case(33)
     ref = run_attention(c, q, table, lens, sb=sb)
