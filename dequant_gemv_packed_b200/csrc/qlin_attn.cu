@@ -51,9 +51,9 @@
 // and the team of an item's first piece a record of it, and a dependent kernel joins
 // the pieces in order, a block a query.  (The last team to arrive joining them by
 // itself was measured slower: one CTA then reads them all, 6 us of 24 at 1 x 32773
-// tokens.)  Otherwise items stay whole and a team has as few warps as keep all teams
-// busy, down to one: nothing is joined, no barrier is needed.  A team's warps take
-// every T-th tile of its piece, each with its own statistics, joined in shared memory.
+// tokens.)  Otherwise items stay whole, nothing is joined, and a team has the two, four
+// or eight warps that an estimate says end first.  A team's warps take every T-th tile
+// of its piece, each with its own statistics, joined in shared memory.
 //
 // A tile is brought in by its warp alone: 16-byte asynchronous copies into the
 // warp's own ring of stages, swizzled so that both the K reads (rows g, g + 8,
@@ -78,9 +78,9 @@ constexpr int kSms = 148;
 constexpr float kNone = -1e30f;   // running maximum of a warp that has seen no token
 constexpr int kWholeTiles = 32;   // items up to here are not cut
 constexpr int kMinShare = 16;     // tiles a team when they are
-// An item's cost beside its tiles, in tiles, for a team of T warps: fitted to 1,592 items of up to 32
-// tiles (29.3, 24.5, 24.3 and 33.4 us with one, two, four and eight warps) and to 16 long sequences
-// among short ones (28.3 us at 16 for eight warps, 24.7 at 24, 24.7 at 32).
+// An item's cost beside its tiles, in tiles, for a team of T warps, fitted to short sequences (200 of
+// up to 509 tokens, 4 bits: 24.2 us; 25.7 with half the slope, 25.3 with 2 + 4 T) and to long ones
+// (24 x 9,000 tokens of 8 heads: 30.9, 38.3 and 31.5 us).
 __device__ __forceinline__ int item_extra(int lt) { return 4 + (4 << lt); }
 // A warp's sums in shared memory: 16 values every 20 floats, which spreads both the lanes that
 // write (16 dimensions of a query each) and those that read over the banks.
@@ -141,6 +141,11 @@ struct AttnArgs {
   int32_t may_cut;                         // the table has room for more than kWholeTiles tiles
 };
 
+// log2 of the least team's warps.  Without a team of two, 400 sequences of up to 60 tokens take 24.3 us
+// and not 18.7; without the choice a team's size would be a constant of the 4-warp shapes (100 x 500,
+// 256 wide: 24.9 and not 26.6).  A team of one: 21.5 and not 20.1 at 400 x 60, 57.3 and not 60.1 at
+// 1,000 x 130, for a longer code.
+constexpr int kMinTeam = 1;
 constexpr int kLensCached = 512;
 
 // Tokens and tiles of sequence b; `lens` holds the first kLensCached of a block's.
@@ -185,13 +190,16 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
   p.cut = a.may_cut && top > kWholeTiles;
   p.lt = 31 - __clz(warps);
   if (!p.cut) {
-    // the longest item on one team, or all items on all warps, in tiles of a warp: the least
-    const float per_warp = rcp((float)(grid * warps));
+    // the longest item on one team, or as many as a team gets of the average one, in tiles of a
+    // warp: the least.  Whole numbers of items: 64 sequences of up to 300 tokens take 10.2 us, 12.8
+    // by the sum of the costs over all warps.
+    const float mean = live ? (float)(n * a.items) * rcp((float)live) : 0.f;
     float best = INFINITY;
 #pragma unroll
-    for (int lt = 31 - __builtin_clz(warps); lt >= 0; --lt) {
+    for (int lt = 31 - __builtin_clz(warps); lt >= kMinTeam; --lt) {
       const int e = item_extra(lt);
-      const float cost = fmaxf((float)(top + e) / (float)(1 << lt), (float)(n * a.items + live * e) * per_warp);
+      const float each = ceilf((float)live * rcp((float)(grid * (warps >> lt))));
+      const float cost = fmaxf((float)(top + e), each * (mean + (float)e)) / (float)(1 << lt);
       if (cost < best) best = cost, p.lt = lt;
     }
   }
@@ -391,7 +399,7 @@ __device__ __forceinline__ void rotate4(float (&v)[4], const uint32_t* sign_bits
 }
 
 // One group of one head's finished sums on a warp: rotated back and stored.
-__device__ __forceinline__ void store_out4(const AttnArgs& a, const uint32_t* signs, int row, int dim, int g, int lane,
+__device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* signs, int row, int dim, int g, int lane,
                                            float (&r)[4], float den) {
   const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
@@ -404,85 +412,20 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, const uint32_t* si
   *reinterpret_cast<uint2*>(a.out + (int64_t)row * dim + g * kGroup + 4 * lane) = w;
 }
 
-// One group of one head's finished sums on eight lanes: rotated back and stored.
-__device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* signs, bool live, int row, int dim, int g,
-                                          int t, const float (&r)[16], float den) {
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  f32x2 v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = pair2(r[2 * i] * inv, r[2 * i + 1] * inv);
-  uint4 h[2];
-  if (a.sign_bits) fwht128<8>(v, t);
-  float_to_halves(v, h);
-  if (a.sign_bits) flip(h[0], sign_mask<8>(signs + 4 * g, t, 0)), flip(h[1], sign_mask<8>(signs + 4 * g, t, 1));
-  if (!live) return;
-  uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)row * dim + g * kGroup) + t;
-  out[0] = h[0], out[8] = h[1];
-}
-
-// Prepares group g of a query (rotation, fp16, digits or halves) in its team's shared
-// operand, eight lanes a group (lane t: dimensions 8 t .. 8 t + 7 and 64 on).
-//   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim], at 4
-//   bits the dimensions of each eight in the order 0 2 4 6 1 3 5 7 (a word's even codes, its odd).
-template <int KB, int NG>
-__device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t* signs, uint4 r0, uint4 r1, int q, int g,
-                                              int t, uint8_t* sq, float2* sx) {
-  constexpr int D = NG * kGroup;
-  f32x2 p[8];
-  uint4 h[2] = {r0, r1};
-  if (a.sign_bits) {
-    flip(h[0], sign_mask<8>(signs + 4 * g, t, 0)), flip(h[1], sign_mask<8>(signs + 4 * g, t, 1));
-    halves_to_float(h, p);
-    fwht128<8>(p, t);
-    float_to_halves(p, h);
-  }
-  if (KB == 16) {
-    uint4* dst = reinterpret_cast<uint4*>(sq + (q * D + g * kGroup) * 2) + t;
-    dst[0] = h[0], dst[8] = h[1];
-    if (t == 0) sx[q * NG + g] = make_float2(a.scale_log2e, 0.f);
-    return;
-  }
-  halves_to_float(h, p);
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) split2(p[i], v[2 * i], v[2 * i + 1]);
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-  const int e = (int)(big >> 23) - 127;  // exponent of the largest (a half is a normal float, or 0)
-  const float down = big ? __uint_as_float((uint32_t)(127 + 13 - e) << 23) : 0.f;
-  uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-  int sum = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int xi = __float2int_rn(v[i] * down), up = xi + 128;  // xi = 256 (up >> 8) + (up & 255) - 128
-    sum += xi;
-    // 4 bits: bytes 0 2 4 6 of an eight, then 1 3 5 7
-    const int at = KB == 8 ? i : (i & 8) + ((i & 1) << 2) + ((i & 7) >> 1);
-    hi[at >> 2] |= (uint32_t)((up >> 8) & 255) << (8 * (at & 3));
-    lo[at >> 2] |= (uint32_t)((up & 255) ^ 128) << (8 * (at & 3));
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  uint2* row = reinterpret_cast<uint2*>(sq + (2 * q) * D + g * kGroup) + t;
-  row[0] = make_uint2(hi[0], hi[1]), row[8] = make_uint2(hi[2], hi[3]);
-  row[D / 8] = make_uint2(lo[0], lo[1]), row[D / 8 + 8] = make_uint2(lo[2], lo[3]);
-  // the sums of 4-bit codes are kept times 16; a query with an infinity or NaN has no scale
-  const float unit = KB == 4 ? 0.0625f : 1.f, step = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-  const float f = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : big ? a.scale_log2e * step * unit : 0.f;
-  if (t == 0) sx[q * NG + g] = make_float2(f, (float)sum / unit);
-}
-
-// Sums of query j, dimensions 4 lane .. 4 lane + 3 of a group, over a team's warps.
-__device__ __forceinline__ void gather4(const uint8_t* smem, const int* dump_at, const float2* sml, int T, int j,
+// Sums of query j, dimensions 4 lane .. 4 lane + 3 of a group, over a team's T of at most W warps.
+// Unrolled, so that the loads do not wait for one another: the call of 1 x 32,773 tokens takes 15.6 us
+// and not 16.5, that of 7 of 256 dimensions and eight queries 26.7 and not 30.4.
+template <int W>
+__device__ __forceinline__ void gather(const uint8_t* smem, const int* dump_at, const float2* sml, int T, int j,
                                         int lane, float (&r)[4], float& top, float& den) {
   top = kNone, den = 0.f;
   r[0] = r[1] = r[2] = r[3] = 0.f;
-  for (int w = 0; w < T; ++w) top = fmaxf(top, sml[w * 4 + j].x);
-#pragma unroll 4
-  for (int w = 0; w < T; ++w) {
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if (w < T) top = fmaxf(top, sml[w * 4 + j].x);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w >= T) break;
     const float2 ml = sml[w * 4 + j];
     const float f = ex2(ml.x - top);
     const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + dump_at[w]) + j * kDumpRow +
@@ -492,10 +435,12 @@ __device__ __forceinline__ void gather4(const uint8_t* smem, const int* dump_at,
   }
 }
 
-// The same on a whole warp (lane: dimensions 4 lane .. 4 lane + 3): shorter, for teams that have a
-// warp for each query.
+// Prepares group g of a query (rotation, fp16, digits or halves) in its team's shared operand, on a
+// warp (lane: dimensions 4 lane .. 4 lane + 3).
+//   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim], at 4
+//   bits the dimensions of each eight in the order 0 2 4 6 1 3 5 7 (a word's even codes, its odd).
 template <int KB, int NG>
-__device__ __forceinline__ void prepare_query4(const AttnArgs& a, const uint32_t* signs, uint2 r, int q, int g, int lane, uint8_t* sq,
+__device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t* signs, uint2 r, int q, int g, int lane, uint8_t* sq,
                                                float2* sx) {
   constexpr int D = NG * kGroup;
   float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
@@ -570,10 +515,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   float2* sx = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ) + team * C::kRowQ * NG;
   float2* sml = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ + C::kSmemX) + (warp - tw) * 4;
   auto team_barrier = [&]() {
-    if (lt)
-      named_barrier(1 + team, 32 << lt);
-    else
-      __syncwarp();
+    named_barrier(1 + team, 32 << lt);
   };
 
   const int64_t begin = (int64_t)worker * plan.share;
@@ -595,24 +537,15 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     if (lane == 0) place[warp][0] = place[warp][1] = cur;
   }
   bool have = more;
-  // the warp's part of a segment's queries: a (query, group) on the warp if the team has a warp for
-  // each of four, else four of them on eight lanes each
-  uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0;
-  auto load_query = [&](int i) {
-    const int j = lt >= 2 ? i : 4 * i + (lane >> 3), q = j / NG;
-    q0 = q1 = make_uint4(0u, 0u, 0u, 0u);
-    if (q < seg.nq) {
-      const __half* src = a.q + (int64_t)seg.b * a.q_stride + (int64_t)(seg.hq0 + q) * D + (j % NG) * kGroup;
-      if (lt >= 2) {
-        const uint2 r = reinterpret_cast<const uint2*>(src)[lane];
-        q0.x = r.x, q0.y = r.y;
-      } else {
-        q0 = reinterpret_cast<const uint4*>(src)[lane & 7];
-        q1 = reinterpret_cast<const uint4*>(src)[(lane & 7) + 8];
-      }
-    }
+  // the warp's part of a segment's queries, a (query, group) at a time
+  uint2 qr = make_uint2(0u, 0u);
+  const auto load_query = [&](int i) {
+    const int q = i / NG;
+    return q < seg.nq ? reinterpret_cast<const uint2*>(a.q + (int64_t)seg.b * a.q_stride + (int64_t)(seg.hq0 + q) * D +
+                                                       (i % NG) * kGroup)[lane]
+                      : make_uint2(0u, 0u);
   };
-  if (have) load_query(tw);
+  if (have) qr = load_query(tw);
 
   // ---- copies: tile ik of icnt of the warp's piece of the segment that they have reached
   int ik = 0, icnt = have && tw < seg.n ? (seg.n - tw + T - 1) >> lt : 0;
@@ -704,14 +637,10 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     const int cnt = tw < seg.n ? (seg.n - tw + T - 1) >> lt : 0;
     // ---- the queries, and the lane's operand: column g8 = (query g8 / 2, digit g8 % 2), the
     // dimensions of the codes that lanes of column t4 hold
-    for (int i = tw; i < (lt >= 2 ? C::kRowQ * NG : NT * NG); i += T) {
-      if (i != tw) load_query(i);
-      if (lt >= 2) {
-        prepare_query4<KB, NG>(a, signs, make_uint2(q0.x, q0.y), i / NG, i % NG, lane, sq, sx);
-      } else {
-        const int j = 4 * i + (lane >> 3);
-        prepare_query<KB, NG>(a, signs, q0, q1, j / NG, j % NG, lane & 7, sq, sx);
-      }
+    for (int i = tw; i < C::kRowQ * NG; i += T) {
+      const uint2 r = qr;
+      if (i + T < C::kRowQ * NG) qr = load_query(i + T);
+      prepare_query<KB, NG>(a, signs, r, i / NG, i % NG, lane, sq, sx);
     }
     team_barrier();
     constexpr int NB = KB == 16 ? 16 : 8;  // operand registers a group
@@ -995,41 +924,18 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         }
         if (g8 == 0) sml[tw * 4 + t4] = make_float2(m[s][g], l[s][g]);
         team_barrier();
-        if (lt >= 2) {
-          for (int j = tw; j < 4; j += T)
-            if (query(s, j) < seg.nq) {
-              float r[4], top, den;
-              gather4(smem, dump_at + warp - tw, sml, T, j, lane, r, top, den);
-              if (seg.n == seg.nt) {
-                store_out4(a, signs, seg.b * a.q_heads + seg.hq0 + query(s, j), D, g, lane, r, den);
-              } else {
-                float* to = a.ws + (((int64_t)worker * 2 + slot) * a.qper + query(s, j)) * (D + 4);
-                __stcg(reinterpret_cast<float4*>(to + g * kGroup + 4 * lane), make_float4(r[0], r[1], r[2], r[3]));
-                if (lane == 0) __stcg(reinterpret_cast<float2*>(to + D + 2 * g), make_float2(top, den));
-              }
-            }
-        } else if (tw == 0) {  // four queries on eight lanes each
-          const int j = lane >> 3, c8 = lane & 7;
-          float top = kNone, den = 0.f, r[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) r[c] = 0.f;
-          for (int w = 0; w < T; ++w) top = fmaxf(top, sml[w * 4 + j].x);
-          for (int w = 0; w < T; ++w) {
-            const float2 ml = sml[w * 4 + j];
-            const float f = ex2(ml.x - top);
-            const float4* from = reinterpret_cast<const float4*>(
-                reinterpret_cast<const float*>(smem + dump_at[warp - tw + w]) + j * kDumpRow + 20 * (c8 >> 1) +
-                8 * (c8 & 1));
-            den = fmaf(f, ml.y, den);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float4 v = from[(c & 1) + 20 * (c >> 1)];  // dimensions 8 c8 .., then 64 on
-              r[4 * c] = fmaf(f, v.x, r[4 * c]), r[4 * c + 1] = fmaf(f, v.y, r[4 * c + 1]);
-              r[4 * c + 2] = fmaf(f, v.z, r[4 * c + 2]), r[4 * c + 3] = fmaf(f, v.w, r[4 * c + 3]);
+        for (int j = tw; j < 4; j += T)
+          if (query(s, j) < seg.nq) {
+            float r[4], top, den;
+            gather<NW>(smem, dump_at + warp - tw, sml, T, j, lane, r, top, den);
+            if (seg.n == seg.nt) {
+              store_out(a, signs, seg.b * a.q_heads + seg.hq0 + query(s, j), D, g, lane, r, den);
+            } else {
+              float* to = a.ws + (((int64_t)worker * 2 + slot) * a.qper + query(s, j)) * (D + 4);
+              __stcg(reinterpret_cast<float4*>(to + g * kGroup + 4 * lane), make_float4(r[0], r[1], r[2], r[3]));
+              if (lane == 0) __stcg(reinterpret_cast<float2*>(to + D + 2 * g), make_float2(top, den));
             }
           }
-          store_out(a, signs, query(s, j) < seg.nq, seg.b * a.q_heads + seg.hq0 + query(s, j), D, g, c8, r, den);
-        }
         team_barrier();  // the stage, the statistics and the queries may be overwritten
       }
 
@@ -1038,7 +944,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     have = next_segment(a, plan, lens, cur, end, seg);
     if (lane == 0) place[warp][1] = cur;
     __syncwarp();
-    if (have) load_query(tw);
+    if (have) qr = load_query(tw);
   }
   cp_wait<0>();
 
@@ -1117,7 +1023,7 @@ __global__ void __launch_bounds__(W * 32) attn_join_kernel(const __grid_constant
       d = fmaf(f, ml.y, d);
       v[0] = fmaf(f, s.x, v[0]), v[1] = fmaf(f, s.y, v[1]), v[2] = fmaf(f, s.z, v[2]), v[3] = fmaf(f, s.w, v[3]);
     }
-    store_out4(a, a.sign_bits, rec.x + q, D, g, lane, v, d);
+    store_out(a, a.sign_bits, rec.x + q, D, g, lane, v, d);
   }
 }
 
