@@ -105,8 +105,8 @@ struct Cfg {
   static constexpr int kAlign = KB == 16 ? 256 : 128;
   static constexpr int kStage = ((kTileBytes > kDump ? kTileBytes : kDump) + 16 + kAlign - 1) / kAlign * kAlign;
   // 32 sums a lane (one group) leave room for 16 warps an SM at 128 registers; 64 (two) for 12 at
-  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 31.0 us; at 168 with
-  // spills 44.1, two passes of four queries 33.0).  16-bit rows fill the rings: 8 warps.
+  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 26.7 us; when it was
+  // chosen 31.0, at 168 with spills 44.1, by two passes of four queries 33.0).  16-bit rows fill the rings: 8 warps.
   static constexpr int kSets = NG;
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
   static constexpr int kSmemQ = kWarps * NT * NG * 1024;        // operand of the queries, a team
