@@ -6,11 +6,15 @@
 //   score_t = c s_k (sum_d q_k x - z_k sum_d x),   c = scale log2(e),
 //   out_d   = sum_t w_t s_v (q_v - z_v) / sum_t w_t,   w_t = 2^(score_t - m).
 // Scores of 4- and 8-bit keys are integer products, m16n8k32 of u8 codes and s8
-// digits: per query and group x is xi 2^(E-13), E the exponent of the largest
-// |x|, xi = 256 hi + lo (values within a factor 8 of the largest are exact, others
-// rounded at 2^-14 of it, as in the M = 1 integer GEMV); sum q xi and sum xi are
-// exact in int32.  The codes are the operand as stored (8 bits) or masked in place
-// (4 bits; the odd codes are 16 q in accumulators of their own).
+// digits: per query and group x is xi 2^(E-21), E the exponent of the largest
+// |x|, xi = 2^16 hi + 2^8 mid + lo (fp16 values within a factor 2^11 of the largest
+// are exact, others rounded at 2^-22 of it, the rounding of an fp32 sum); each digit's
+// sum of products and sum xi are exact in int32, and the digits' sums meet in fp32.
+// Two digits, 2^-14 of the largest, would lose the small channels of a query with a large
+// one and move every output by 0.8e-4; the third costs four products a tile and group, 5 %
+// of the time where products bind (32 x 8,000 tokens, 8 bits: 93.5 us, 88.4 with two; 4 bits:
+// 62.6, 56.8).  The codes are the operand as stored (8 bits)
+// or masked in place (4 bits; the odd codes are 16 q in accumulators of their own).
 // Values: a nibble or byte masked into the low bits of an fp16 word is the
 // subnormal fp16 number q 2^-24 (a nibble at bits 4-7: q 2^-20), and one packed
 // multiplication makes a pair q 2^-9, exact.  (The subnormals would be exact
@@ -25,13 +29,13 @@
 //
 // The eight columns of the products.  S^T = K Q^T has the tile's 16 tokens as rows,
 // O^T = V^T P^T 16 dimensions; lane (g, t) of an accumulator has columns 2t, 2t + 1.
-// Up to four queries (NT = 1): the columns are (query, digit) pairs in both, so a
-// lane has the scores of query t for tokens g and g + 8 (none is padding at the usual
-// four queries a key), and P enters the value sums as two fp16 digits, hi + 2^-11 lo
-// (22 bits), packed as they are.
-// Five to eight queries (NT = 2): the keys' products take a second set of (query,
-// digit) columns (16-bit keys: one set of eight queries), with queries 2t and 2t + 1
-// in lane t, and the columns of the value sums are the eight queries: P is one fp16
+// Up to four queries (NT = 1): the columns are (query, digit) pairs in both (the keys'
+// lowest digits take a second set, every other column unused), so a lane has the scores of
+// query t for tokens g and g + 8 (none is padding at the usual four queries a key), and P
+// enters the value sums as two fp16 digits, hi + 2^-11 lo (22 bits), packed as they are.
+// Five to eight queries (NT = 2): the keys' products take two sets of (query, digit)
+// columns and one of the eight lowest digits (16-bit keys: one set of eight queries), with
+// queries 2t and 2t + 1 in lane t, and the columns of the value sums are the eight queries: P is one fp16
 // number.  Its rounding, 2^-12 of a weight, stands in the zero's share and the
 // denominator too, so that it moves the weights and not their normalisation (a
 // subnormal P, 2^21 below the largest, enters the denominator unrounded: a token with
@@ -93,6 +97,12 @@ constexpr int kItemRecords = 64;
 static_assert(kItemRecords <= kMaxTeams);
 constexpr int kRecordBytes = kMaxTeams * 16;  // of the workspace: the item that each team is the first to cut
 
+// log2 of the least team's warps.  Without a team of two, 400 sequences of up to 60 tokens take 24.3 us
+// and not 18.7; without the choice a team's size would be a constant of the 4-warp shapes (100 x 500,
+// 256 wide: 24.9 and not 26.6).  A team of one: 21.5 and not 20.1 at 400 x 60, 57.3 and not 60.1 at
+// 1,000 x 130, for a longer code.
+constexpr int kMinTeam = 1;
+
 template <int KB, int VB, int NG, int NT>
 struct Cfg {
   static constexpr int kDim = NG * kGroup;
@@ -109,8 +119,13 @@ struct Cfg {
   // chosen 31.0, at 168 with spills 44.1, by two passes of four queries 33.0).  16-bit rows fill the rings: 8 warps.
   static constexpr int kSets = NG;
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
-  static constexpr int kSmemQ = kWarps * NT * NG * 1024;        // operand of the queries, a team
-  static constexpr int kSmemX = kWarps * kRowQ * NG * 8;        // (scale, sum) of each, a team
+  static constexpr int kPlanes = 1024 * NT * NG;                // halves of the queries, or their two upper digits
+  static constexpr int kOperand = KB == 16 ? kPlanes : kPlanes + kPlanes / 2;  // and the lowest digits
+  // Whether the lowest digits stay in registers through the tiles: 32 x 8,000 tokens at 4 bits take 62.6 us
+  // and not 64.8; the other shapes would spill.
+  static constexpr bool kLowHeld = KB < 16 && NT == 1 && NG == 1;
+  static constexpr int kSmemQ = (kWarps >> kMinTeam) * kOperand;          // of each team
+  static constexpr int kSmemX = (kWarps >> kMinTeam) * kRowQ * NG * 8;    // (scale, sum) of each query, a team
   static constexpr int kSmemMl = kWarps * 4 * 8;                // (m, l) of four queries, a warp
   static constexpr int kOther = kSmemQ + kSmemX + kSmemMl + kAlign;  // and room to align it
   static constexpr int fit(int ctas) { return (226 * 1024 / ctas - 4096 - kOther) / (kWarps * kStage); }
@@ -141,11 +156,6 @@ struct AttnArgs {
   int32_t may_cut;                         // the table has room for more than kWholeTiles tiles
 };
 
-// log2 of the least team's warps.  Without a team of two, 400 sequences of up to 60 tokens take 24.3 us
-// and not 18.7; without the choice a team's size would be a constant of the 4-warp shapes (100 x 500,
-// 256 wide: 24.9 and not 26.6).  A team of one: 21.5 and not 20.1 at 400 x 60, 57.3 and not 60.1 at
-// 1,000 x 130, for a longer code.
-constexpr int kMinTeam = 1;
 constexpr int kLensCached = 512;
 
 // Tokens and tiles of sequence b; `lens` holds the first kLensCached of a block's.
@@ -437,9 +447,11 @@ __device__ __forceinline__ void gather(const uint8_t* smem, const int* dump_at, 
 
 // Prepares group g of a query (rotation, fp16, digits or halves) in its team's shared operand, on a
 // warp (lane: dimensions 4 lane .. 4 lane + 3).
-//   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim], at 4
-//   bits the dimensions of each eight in the order 0 2 4 6 1 3 5 7 (a word's even codes, its odd).
-template <int KB, int NG>
+//   16-bit keys: halves of query q at [q][dim]; below: digit planes [2 q + digit][dim] of the two
+//   upper digits, then [q][dim] of the lowest, at 4 bits the dimensions of each eight in the order
+//   0 2 4 6 1 3 5 7 (a word's even codes, its odd).  The lowest digits of odd queries change places
+//   in blocks of 64 (4 bits: 16) bytes, so that the lanes that read them meet no bank conflict.
+template <int KB, int NG, int NT>
 __device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t* signs, uint2 r, int q, int g, int lane, uint8_t* sq,
                                                float2* sx) {
   constexpr int D = NG * kGroup;
@@ -464,29 +476,35 @@ __device__ __forceinline__ void prepare_query(const AttnArgs& a, const uint32_t*
   for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(v[i]) & 0x7fffffffu);
   big = __reduce_max_sync(0xffffffffu, big);
   const int e = (int)(big >> 23) - 127;
-  const float down = big ? __uint_as_float((uint32_t)(127 + 13 - e) << 23) : 0.f;
+  const float down = big ? __uint_as_float((uint32_t)(127 + 21 - e) << 23) : 0.f;
   int sum = 0;
-  uint32_t hi = 0, lo = 0;
+  uint32_t hi = 0, mid = 0, lo = 0;  // digits of -128 .. 127, |hi| <= 64
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int xi = __float2int_rn(v[i] * down), up = xi + 128;
-    sum += xi;
-    hi |= (uint32_t)((up >> 8) & 255) << (8 * i);
+    const int xi = __float2int_rn(v[i] * down), up = xi + 128, upper = (up >> 8) + 128;
+    sum += xi;  // at most 128 2^22
+    hi |= (uint32_t)((upper >> 8) & 255) << (8 * i);
+    mid |= (uint32_t)((upper & 255) ^ 128) << (8 * i);
     lo |= (uint32_t)((up & 255) ^ 128) << (8 * i);
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
   uint8_t* row = sq + (2 * q) * D + g * kGroup;
+  uint8_t* low = sq + 1024 * NT * NG + q * D + g * kGroup;
   if (KB == 8) {
     *reinterpret_cast<uint32_t*>(row + 4 * lane) = hi;
-    *reinterpret_cast<uint32_t*>(row + D + 4 * lane) = lo;
+    *reinterpret_cast<uint32_t*>(row + D + 4 * lane) = mid;
+    *reinterpret_cast<uint32_t*>(low + ((4 * lane) ^ (64 * (q & 1)))) = lo;
   } else {  // dimensions 4l .. 4l+3 of an eight: its bytes 2 (l & 1), + 1 (even) and 4 bytes on (odd)
     row += 8 * (lane >> 1) + 2 * (lane & 1);
     *reinterpret_cast<uint16_t*>(row) = (uint16_t)__byte_perm(hi, 0, 0x4420);
     *reinterpret_cast<uint16_t*>(row + 4) = (uint16_t)__byte_perm(hi, 0, 0x4431);
-    *reinterpret_cast<uint16_t*>(row + D) = (uint16_t)__byte_perm(lo, 0, 0x4420);
-    *reinterpret_cast<uint16_t*>(row + D + 4) = (uint16_t)__byte_perm(lo, 0, 0x4431);
+    *reinterpret_cast<uint16_t*>(row + D) = (uint16_t)__byte_perm(mid, 0, 0x4420);
+    *reinterpret_cast<uint16_t*>(row + D + 4) = (uint16_t)__byte_perm(mid, 0, 0x4431);
+    low += (8 * (lane >> 1) + 2 * (lane & 1)) ^ (16 * (q & 1));
+    *reinterpret_cast<uint16_t*>(low) = (uint16_t)__byte_perm(lo, 0, 0x4420);
+    *reinterpret_cast<uint16_t*>(low + 4) = (uint16_t)__byte_perm(lo, 0, 0x4431);
   }
-  const float unit = KB == 4 ? 0.0625f : 1.f, step = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+  const float unit = KB == 4 ? 0.0625f : 1.f, step = __uint_as_float((uint32_t)(127 - 21 + e) << 23);
   const float f = big >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : big ? a.scale_log2e * step * unit : 0.f;
   if (lane == 0) sx[q * NG + g] = make_float2(f, (float)sum / unit);
 }
@@ -511,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   const Plan plan = make_plan<NW * 32>(a, lens, grid);
   const int lt = plan.lt, T = 1 << lt, team = warp >> lt, tw = warp & (T - 1);
   const int teams = NW >> lt, worker = blockIdx.x * teams + team;
-  uint8_t* sq = smem + C::kRing + team * (NT * NG * 1024);
+  uint8_t* sq = smem + C::kRing + team * C::kOperand;
   float2* sx = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ) + team * C::kRowQ * NG;
   float2* sml = reinterpret_cast<float2*>(smem + C::kRing + C::kSmemQ + C::kSmemX) + (warp - tw) * 4;
   auto team_barrier = [&]() {
@@ -522,6 +540,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   const int end = (int)min((int64_t)plan.total, begin + plan.share);
   __shared__ int4 place[NW][2];      // a warp's places: of its copies, of its sums
   __shared__ int dump_at[NW];        // where a warp's sums are, in bytes
+  __shared__ Segment held[NW];       // a warp's segment, out of the registers while it reads the tiles
   int4 record = make_int4(0, 0, 0, 0);
   bool more = begin < plan.total;
   Segment seg = {};
@@ -633,6 +652,10 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
                          (VB == 4   ? v_at<VB>(2 * t4, g8 >> 1) + 8 * (g8 & 1)
                           : VB == 8 ? v_at<VB>(2 * t4, g8)
                                     : v_at<VB>((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1));
+  // the lowest digits of column g8's query: the second piece at ^ (KB == 4 ? 16 : 64)
+  const int low_q = NT == 1 ? g8 >> 1 : g8;
+  const uint32_t low_src = smem_addr(sq) + C::kPlanes + low_q * D +
+                           (KB == 4 ? 32 * t4 + 16 * (low_q & 1) : 16 * t4 + 64 * (low_q & 1));
   while (have) {
     const int cnt = tw < seg.n ? (seg.n - tw + T - 1) >> lt : 0;
     // ---- the queries, and the lane's operand: column g8 = (query g8 / 2, digit g8 % 2), the
@@ -640,12 +663,14 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     for (int i = tw; i < C::kRowQ * NG; i += T) {
       const uint2 r = qr;
       if (i + T < C::kRowQ * NG) qr = load_query(i + T);
-      prepare_query<KB, NG>(a, signs, r, i / NG, i % NG, lane, sq, sx);
+      prepare_query<KB, NG, NT>(a, signs, r, i / NG, i % NG, lane, sq, sx);
     }
     team_barrier();
     constexpr int NB = KB == 16 ? 16 : 8;  // operand registers a group
     constexpr int NS = KB == 16 ? 1 : NT;  // column sets of the keys' products
     uint32_t qf[NS][NG][NB];
+    uint4 qlow[2];
+    if (C::kLowHeld) qlow[0] = ld128(low_src), qlow[1] = ld128(low_src ^ (KB == 4 ? 16 : 64));
     float xs[NT][NG], sc[NT][NG];  // sum and scale of query(s, t4)
     const auto query = [](int s, int t) { return NT == 1 ? t : 2 * t + s; };
 #pragma unroll
@@ -684,6 +709,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
       }
     }
 
+    if (lane == 0) held[warp] = seg;
     for (int k = 0; k < cnt; ++k) {
       cp_wait<S - 2>();
       __syncwarp();
@@ -705,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         if (KB == 4) {
           const uint4 wa = ld128(kb), wb = ld128(kb + 128 * KB);
           const uint32_t ra[4] = {wa.x, wa.y, wa.z, wa.w}, rb[4] = {wb.x, wb.y, wb.z, wb.w};
-          int c0[NT][4], c1[NT][4];
+          int c0[NT][4], c1[NT][4], e0[4] = {0, 0, 0, 0}, e1[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int s = 0; s < NT; ++s)
 #pragma unroll
@@ -713,6 +739,9 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
             constexpr uint32_t lo = 0x0F0F0F0Fu, hi = 0xF0F0F0F0u;
+            const uint4 x = C::kLowHeld ? qlow[j / 2] : ld128((low_src + g * kGroup) ^ (8 * j));
+            imma(e0, ra[j] & lo, rb[j] & lo, ra[j + 1] & lo, rb[j + 1] & lo, x.x, x.z);
+            imma(e1, ra[j] & hi, rb[j] & hi, ra[j + 1] & hi, rb[j + 1] & hi, x.y, x.w);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
               imma(c0[s], ra[j] & lo, rb[j] & lo, ra[j + 1] & lo, rb[j + 1] & lo, qf[s % NS][g][2 * j], qf[s % NS][g][2 * j + 2]);
@@ -724,9 +753,10 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           for (int s = 0; s < NT; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              dot[s][i] = (float)((16 * c0[s][2 * i] + c1[s][2 * i]) * 256 + (16 * c0[s][2 * i + 1] + c1[s][2 * i + 1]));
+              dot[s][i] = fmaf((float)((16 * c0[s][2 * i] + c1[s][2 * i]) * 256 + (16 * c0[s][2 * i + 1] + c1[s][2 * i + 1])),
+                               256.f, (float)(16 * e0[2 * i + s] + e1[2 * i + s]));
         } else if (KB == 8) {
-          int c0[NT][4], c1[NT][4];
+          int c0[NT][4], c1[NT][4], e[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int s = 0; s < NT; ++s)
 #pragma unroll
@@ -734,6 +764,9 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 wa = ld128(kb ^ (64 * j)), wb = ld128((kb ^ (64 * j)) + 128 * KB);
+            const uint4 x = C::kLowHeld ? qlow[j] : ld128((low_src + g * kGroup) ^ (64 * j));
+            imma(e, wa.x, wb.x, wa.y, wb.y, x.x, x.y);
+            imma(e, wa.z, wb.z, wa.w, wb.w, x.z, x.w);
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
               imma(c0[s], wa.x, wb.x, wa.y, wb.y, qf[s % NS][g][4 * j], qf[s % NS][g][4 * j + 1]);
@@ -744,7 +777,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           for (int s = 0; s < NT; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-              dot[s][i] = (float)((c0[s][2 * i] + c1[s][2 * i]) * 256 + (c0[s][2 * i + 1] + c1[s][2 * i + 1]));
+              dot[s][i] = fmaf((float)((c0[s][2 * i] + c1[s][2 * i]) * 256 + (c0[s][2 * i + 1] + c1[s][2 * i + 1])), 256.f,
+                               (float)e[2 * i + s]);
         } else {
           float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -883,6 +917,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
       }
     }
     __syncwarp();  // every lane has read the last tile, and its stage is free
+    seg = held[warp];
 
     // ---- the sums of four queries and one group at a time: each warp's into its free stage, then the
     // team's

@@ -438,9 +438,9 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  * kv_heads), x = fp16_rn(R q[b][h]) and R the rotation (R = 1 and x = q[b][h]
  * without sign bits; the codes then are those of unrotated vectors).  Scores,
  * softmax statistics and sums are fp32.  For 4- and 8-bit keys x enters the scores
- * as 16-bit integers with one power-of-two scale per group of 128 (exact for values
- * within a factor 8 of the group's largest, others rounded at 2^-14 of it, far
- * below half a step of the keys).  The softmax weights (times the values' scales)
+ * as 24-bit integers with one power-of-two scale per group of 128 (exact for values
+ * within a factor 2^11 of the group's largest, others rounded at 2^-22 of it, as an
+ * fp32 sum would round them).  The softmax weights (times the values' scales)
  * enter the value sums with 22 bits for up to four queries a kv head, above with 11,
  * alike in numerator and denominator.  An infinity or NaN among a head's query, keys or values within the length
  * gives NaN there; what lies past the length has no effect.  Deterministic.

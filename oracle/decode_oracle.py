@@ -151,9 +151,9 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
         so that only its share of |v - out| is moved;
       * a score is 128 or 256 products summed in fp32 (a rounding of 2^-24 of the
         magnitudes per step, sums of code products and of the zero's share apart);
-      * for 4- and 8-bit keys x is rounded to 16-bit integers of unit 2^(E-13), E the
-        exponent of the group's largest |x|: at most 2^-14 max|x| a value, that is
-        2^-14 max|x| sum |k| a score;
+      * for 4- and 8-bit keys x is rounded to 24-bit integers of unit 2^(E-21), E the
+        exponent of the group's largest |x|: at most 2^-22 max|x| a value, that is
+        2^-22 max|x| sum |k| a score;
         a score's error e enters as p e |v - out|, twice that with the exponential's own;
       * the value sums are len products in fp32 over s (q + |z|);
       * everything else (rotation, quotient, joins) is some 64 fp32 steps.
@@ -188,7 +188,7 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
             e = abs(scale) * (mag[0][:, h // g] @ np.abs(x)) * (D + 64) * 2.0 ** -24 + np.abs(s) * 2.0 ** -22
             if coded:
                 for c in range(0, D, GROUP):
-                    e = e + abs(scale) * 2.0 ** -14 * np.abs(x[c:c + GROUP]).max() * np.abs(kh[:, c:c + GROUP]).sum(1)
+                    e = e + abs(scale) * 2.0 ** -22 * np.abs(x[c:c + GROUP]).max() * np.abs(kh[:, c:c + GROUP]).sum(1)
             p = np.exp(s - s.max())
             p /= p.sum()
             o = p @ vh
