@@ -13,8 +13,8 @@
 // Two digits, 2^-14 of the largest, would lose the small channels of a query with a large
 // one and move every output by 0.8e-4; the third costs four products a tile and group, 5 %
 // of the time where products bind (32 x 8,000 tokens, 8 bits: 93.5 us, 88.4 with two; 4 bits:
-// 62.6, 56.8).  The codes are the operand as stored (8 bits)
-// or masked in place (4 bits; the odd codes are 16 q in accumulators of their own).
+// 62.6, 56.8).  The codes are the operand as stored (8 bits) or masked in place (4 bits;
+// the odd codes are 16 q in accumulators of their own).
 // Values: a nibble or byte masked into the low bits of an fp16 word is the
 // subnormal fp16 number q 2^-24 (a nibble at bits 4-7: q 2^-20), and one packed
 // multiplication makes a pair q 2^-9, exact.  (The subnormals would be exact
@@ -35,13 +35,10 @@
 // enters the value sums as two fp16 digits, hi + 2^-11 lo (22 bits), packed as they are.
 // Five to eight queries (NT = 2): the keys' products take two sets of (query, digit)
 // columns and one of the eight lowest digits (16-bit keys: one set of eight queries), with
-// queries 2t and 2t + 1 in lane t, and the columns of the value sums are the eight queries: P is one fp16
-// number.  Its rounding, 2^-12 of a weight, stands in the zero's share and the
-// denominator too, so that it moves the weights and not their normalisation (a
-// subnormal P, 2^21 below the largest, enters the denominator unrounded: a token with
-// a tiny scale may hold most of the weight).  A second digit would need a second set of
-// sums: half the warps an SM, and twice the value products (24 x 9000 tokens of 8 kv
-// heads at 4 bits: 76.7 us with it, 68.2 without).
+// queries 2t and 2t + 1 in lane t, and the columns of the value sums are the eight queries:
+// P's two digits, fp16(P) and fp16(P - fp16(P)), take a product each, into the same sums.
+// (One digit, 11 bits, moved every output by 1.2e-4 for 3 % less time: 24 x 9000 tokens of
+// 8 kv heads at 4 bits 70.0 us, 72.4 with two.)
 // In both movmatrix turns the packed pair into the next product's operand, and a
 // query's statistics live in the lanes that scale its sums.  More than eight queries
 // take another pass over the cache.
@@ -825,7 +822,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           }
       }
 
-      uint32_t pb[NG][2];
+      uint32_t pb[NG][2], pl[NG][2];  // weights as operand; with NT = 2 their second digits
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float y[NT][2], top[NT];
@@ -865,11 +862,12 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 #pragma unroll
             for (int s = 0; s < NT; ++s) p[s] = ex2(y[s][i] - m[s][g]);
             pair = __floats2half2_rn(p[0], p[NT - 1]);
-            const float r[2] = {__low2float(pair), __high2float(pair)};
+            const __half2 rest = __floats2half2_rn(p[0] - __low2float(pair), p[NT - 1] - __high2float(pair));
+            pl[g][i] = movmatrix(*reinterpret_cast<const uint32_t*>(&rest));
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
-              l[s][g] = fmaf(p[s] < 0x1p-14f ? p[s] : r[s], rv[g][i], l[s][g]);
-              if (C::kPar) zc[s][g] = fmaf(r[s], vz[g][i], zc[s][g]);
+              l[s][g] = fmaf(p[s], rv[g][i], l[s][g]);
+              if (C::kPar) zc[s][g] = fmaf(p[s], vz[g][i], zc[s][g]);
             }
           }
           pb[g][i] = movmatrix(*reinterpret_cast<const uint32_t*>(&pair));
@@ -893,6 +891,10 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const uint32_t x1 = high4(x), x3 = high4(x >> 8), y1 = high4(y), y3 = high4(y >> 8);
             mma(o[g][2 * half], x0, x2, y0, y2, pb[g][0], pb[g][1]);
             mma(o[g][2 * half + 1], x1, x3, y1, y3, pb[g][0], pb[g][1]);
+            if (NT == 2) {
+              mma(o[g][2 * half], x0, x2, y0, y2, pl[g][0], pl[g][1]);
+              mma(o[g][2 * half + 1], x1, x3, y1, y3, pl[g][0], pl[g][1]);
+            }
           }
         } else if (VB == 8) {
           uint4 v[4];
@@ -906,12 +908,14 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const uint32_t x = __byte_perm(v0[j >> 1], v1[j >> 1], sel), y = __byte_perm(v2[j >> 1], v3[j >> 1], sel);
             const uint32_t x0 = low8(x), x1 = low8(x >> 8), y0 = low8(y), y1 = low8(y >> 8);
             mma(o[g][j], x0, x1, y0, y1, pb[g][0], pb[g][1]);
+            if (NT == 2) mma(o[g][j], x0, x1, y0, y1, pl[g][0], pl[g][1]);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint4 v = ldmatrix_x4_trans(vb ^ (32 * j));
             mma(o[g][j], v.x, v.y, v.z, v.w, pb[g][0], pb[g][1]);
+            if (NT == 2) mma(o[g][j], v.x, v.y, v.z, v.w, pl[g][0], pl[g][1]);
           }
         }
       }

@@ -146,9 +146,7 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
 
     The tolerance bounds what fp32 scores and 22-bit softmax weights may do:
       * a weight enters the value sums as two fp16 digits: 2^-21 relative, or 2^-32 of
-        the largest for every token (digits that are subnormal); with more than four
-        queries a kv head as one, 2^-11 relative, in numerator and denominator alike,
-        so that only its share of |v - out| is moved;
+        the largest for every token (digits that are subnormal);
       * a score is 128 or 256 products summed in fp32 (a rounding of 2^-24 of the
         magnitudes per step, sums of code products and of the zero's share apart);
       * for 4- and 8-bit keys x is rounded to 24-bit integers of unit 2^(E-21), E the
@@ -193,7 +191,7 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
             p /= p.sum()
             o = p @ vh
             far = np.abs(vh - o)
-            d = (p * (2 * e + 2.0 ** -20 + (2.0 ** -11 if g > 4 else 0))) @ far + 2.0 ** -32 * far.sum(0)
+            d = (p * (2 * e + 2.0 ** -20)) @ far + 2.0 ** -32 * far.sum(0)
             d = d + (t.size + 64) * 2.0 ** -24 * (p @ mag[1][:, h // g]) + 2.0 ** -18 * np.abs(o)
             out[b, h] = R.T @ o
             tol[b, h] = np.abs(R.T) @ d

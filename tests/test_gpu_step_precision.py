@@ -81,3 +81,18 @@ def test_query_of_two_sizes(kb, vb, group, ratio):
     q = 0.05 * np.abs(rng.standard_normal((1, group, 128)))
     q[:, :, large] = 0.06 * ratio
     check(c, q.astype(np.float16), np.zeros((1, 1), int), [2])
+
+
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 8), (8, 4), (4, 8), (16, 16)])
+@pytest.mark.parametrize("dim,group", [(128, 4), (128, 5), (128, 8), (256, 7), (128, 12)])
+def test_weights_of_values_that_cancel(kb, vb, dim, group):
+    """Three tokens whose large values cancel in the sum, so that a rounding of their weights is not hidden by the
+    output's: a weight of 11 bits would be 2^-12 of the values away, one of 22 bits 2^-23."""
+    rng = np.random.default_rng(kb + vb + dim + group)
+    c = D.Cache(1, 16, 1, dim, kb, vb)
+    k = 0.1 * rng.standard_normal((3, 1, dim))
+    v = np.repeat(np.array([1000.0, -800.0, -100.0]).reshape(3, 1, 1), dim, 2) * (1 + 0.1 * rng.random((1, 1, dim)))
+    c.write(k.astype(np.float16), v.astype(np.float16), range(3))
+    q = rng.standard_normal((1, group, dim)).astype(np.float16)
+    ref = check(c, q, np.zeros((1, 1), int), [3])
+    assert np.abs(ref).max() < 200
