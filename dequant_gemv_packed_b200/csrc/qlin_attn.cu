@@ -798,10 +798,11 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 #pragma unroll
             for (int s = 0; s < NT; ++s)
               w[s][i] = fmaf(fmaf(-pk.y, xs[s][g], dot[s][i]), pk.x * sc[s][g], w[s][i]);
-            // a scale of 0 (a slot that was cleared, never written) is 2^-100 here: its token has a
-            // share of the denominator and none of the sums
-            lv[g][i] = fmaxf(lg2(pv.x), -100.f);
-            rv[g][i] = fminf(rcp(pv.x), 0x1p100f);
+            // a scale of 0 (a slot that was cleared, never written) is 2^-64 here: its token has a
+            // share of the denominator and none of the sums.  The denominator of 2^31 such tokens
+            // stays below 2^(15 + 64 + 31), and beside a scale of 2^16 weights down to 2^-53 count.
+            lv[g][i] = fmaxf(lg2(pv.x), -64.f);
+            rv[g][i] = fminf(rcp(pv.x), 0x1p64f);
             vz[g][i] = pv.y;
           } else {
 #pragma unroll

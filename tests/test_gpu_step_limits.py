@@ -1,0 +1,68 @@
+"""The decode-step calls at the ends of what they accept: pages of many gigabytes, and values that are not finite."""
+import numpy as np
+import pytest
+import torch
+
+from dequant_gemv_packed_b200 import qlin as Q
+from oracle import decode_oracle as D
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dequant_gemv_packed_b200 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    Q.lib()
+    yield
+    torch.cuda.empty_cache()  # pools of gigabytes
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    Q.qlin_device_error()
+    yield
+    assert Q.qlin_device_error() == 0
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+@pytest.mark.parametrize("kb,vb,size,log", [(8, 8, 1.0, 22), (4, 4, 1.0, 26), (4, 4, 60000.0, 22), (8, 4, 60000.0, 22)])
+def test_millions_of_cleared_slots(kb, vb, size, log):
+    """A sequence of 2^22 or 2^26 cleared slots (a page that its table names over and over) and 16 written tokens with
+    scores near 12, so that both have a part of the weights; values of ordinary size, and with scales of 2^13.
+
+    A cleared slot stands for k = v = 0: a weight of e^0 in the denominator.  The bound: a score's fp32 error
+    twice, the denominator's fp32 sum in chains of at most 2^log / (148 * 4 * 8) additions and 400 joins, the exponentials,
+    each as a share of sum p |v|; and the output's own rounding."""
+    rng = np.random.default_rng(kb + vb)
+    page, cleared = 256, 1 << log
+    base = np.sign(rng.standard_normal(128))
+    k = (base + 0.1 * rng.standard_normal((16, 1, 128))).astype(np.float16)
+    v = (size * rng.uniform(-1, 1, (16, 1, 128))).astype(np.float16)
+    q = (1.05 * base + 0.05 * rng.standard_normal((1, 4, 128))).astype(np.float16)
+    c = D.Cache(2, page, 1, 128, kb, vb)
+    c.write(k, v, range(page, page + 16))
+    d = Q.KVDesc(2, page, 1, 128, kb, vb)
+    table = np.zeros((1, cleared // page + 1), np.int32)
+    table[0, -1] = 1
+    got = Q.qlin_attn_decode(d, dev(c.bytes.reshape(-1)), dev(q), dev(table), dev(np.array([cleared + 16], np.int32)))
+    kk, vv = (c.values(i, range(page, page + 16))[:, 0].astype(np.float64) for i in (0, 1))
+    scale = float(np.float32(128 ** -0.5))
+    par = c.par[1, 0, :16, 0].astype(np.float64)
+    mag = np.abs(kk) + 2 * np.abs(par[:, :1] * par[:, 1:2])
+    for h in range(4):
+        x = q[0, h].astype(np.float64)
+        s = scale * (kk @ x)
+        assert 10 < s.min() and s.max() < 14
+        e = scale * (mag @ np.abs(x)) * (128 + 64) * 2.0 ** -24 + 2.0 ** -22 * scale * np.abs(x).max() * np.abs(kk).sum(1)
+        p = np.exp(s) / (cleared + np.exp(s).sum())
+        ref = p @ vv
+        chain = (cleared / (148 * 4 * 8) + 400) * 2.0 ** -24
+        tol = (p * (2 * e + chain + 2.0 ** -18)) @ np.abs(vv) + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25
+        err = np.abs(got[0, h].double().cpu().numpy() - ref)
+        assert (err <= tol).all(), f"worst error / bound {float((err / tol).max()):.3f}"
