@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   // ---- copies: tile ik of icnt of the warp's piece of the segment that they have reached
   int ik = 0, icnt = have && tw < seg.n ? (seg.n - tw + T - 1) >> lt : 0;
   int itile = seg.tile0 + tw, ilen = seg.len, ih = seg.h, istage = 0;
-  uint32_t src_lo = 0, src_hi = 0, meta = 0;  // of 32 tiles, one a lane: address of the K rows; offset in the page, tokens
+  uint32_t src_lo = 0, src_hi = 0, meta = 0;  // of 32 tiles, one a lane: address of the K rows; tile in the page, tokens
   // where the lane's first piece goes; piece j goes to (first ^ swizzle(j)) + pitch(j), a constant each
   constexpr int RK = KB * NG, RV = VB * NG;
   const uint32_t k_dst = ring + (lane % RK) / KB * (kTile * 16 * KB) + k_at<KB>(lane / RK, lane % KB);
@@ -601,14 +601,15 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             p = 0;
             valid = 0;
           }
-          const int off = (tile - page * page_tiles) * kTile;
-          const uint64_t src = reinterpret_cast<uint64_t>(a.c.block(p, ih)) + (int64_t)off * C::kRowK;
+          const int at = tile - page * page_tiles;  // below 2^27: a page has fewer than 2^31 tokens
+          const uint64_t src = reinterpret_cast<uint64_t>(a.c.block(p, ih)) + (int64_t)at * (kTile * C::kRowK);
           src_lo = (uint32_t)src, src_hi = (uint32_t)(src >> 32);
-          meta = (uint32_t)off << 5 | (uint32_t)valid;
+          meta = (uint32_t)at << 5 | (uint32_t)valid;
         }
       }
       const uint32_t lo = __shfl_sync(0xffffffffu, src_lo, ik & 31), hi = __shfl_sync(0xffffffffu, src_hi, ik & 31);
-      const uint32_t mt = __shfl_sync(0xffffffffu, meta, ik & 31), valid = mt & 31u, off = mt >> 5;
+      const uint32_t mt = __shfl_sync(0xffffffffu, meta, ik & 31), valid = mt & 31u;
+      const int64_t in_page = mt >> 5;  // tiles; a page may hold more than 2^31 bytes
       const uint8_t* src = reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo) + 16 * lane;
       const uint32_t at = istage * C::kStage;
 #pragma unroll
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         cp16(((k_dst + at) ^ (uint32_t)(k_at<KB>(r, 0) - r * pitch)) + r * pitch, src + 512 * j);
       }
       const uint8_t* v_src = src + a.c.v_offset;
-      if (RV != RK) v_src += (int64_t)((int)off * (C::kRowV - C::kRowK));
+      if (RV != RK) v_src += in_page * (kTile * (C::kRowV - C::kRowK));
 #pragma unroll
       for (int j = 0; j < RV / 2; ++j) {
         constexpr int pitch = 16 * VB;
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
       }
       if (C::kPar) {
         if (lane < kTile * C::kPar / 16)
-          cp16(ring + at + C::kOffPar + 16 * lane, src + a.c.par_offset + (int64_t)((int)off * (C::kPar - C::kRowK)));
+          cp16(ring + at + C::kOffPar + 16 * lane, src + a.c.par_offset + in_page * (kTile * (C::kPar - C::kRowK)));
       }
       if (lane == 0) *reinterpret_cast<uint32_t*>(ring_ptr + at + C::kStage - 16) = valid;
       ++ik;

@@ -66,3 +66,32 @@ def test_millions_of_cleared_slots(kb, vb, size, log):
         tol = (p * (2 * e + chain + 2.0 ** -18)) @ np.abs(vv) + np.abs(ref) * 2.0 ** -11 + 2.0 ** -25
         err = np.abs(got[0, h].double().cpu().numpy() - ref)
         assert (err <= tol).all(), f"worst error / bound {float((err / tol).max()):.3f}"
+
+
+@pytest.mark.parametrize("page,dim,kb,vb", [(9_000_000, 256, 8, 8), (17_000_000, 256, 8, 4), (2 ** 27 + 16, 128, 4, 4)])
+def test_attention_far_inside_one_page(page, dim, kb, vb):
+    """The last tokens of a page of 4.8 to 18.3 GB: offsets from a tile's keys to its values and parameters pass 2^31,
+    and the tile's place in the page 2^23 (2^27 tokens).
+
+    The pool is cleared but for the last 40 tokens.  A cleared slot has a score of 0, those tokens have scores above
+    50, so the others' share of the weights is below 2^28 e^-50 < 1e-13."""
+    rng = np.random.default_rng(dim + kb)
+    n = 40
+    base = np.sign(rng.standard_normal(dim))
+    k = (base + 0.3 * rng.standard_normal((n, 1, dim))).astype(np.float16)
+    v = rng.standard_normal((n, 1, dim)).astype(np.float16)
+    q = (6 * base + rng.standard_normal((1, 4, dim))).astype(np.float16)
+    d = Q.KVDesc(1, page, 1, dim, kb, vb)
+    pool = torch.zeros(Q.qlin_kv_cache_bytes(d), dtype=torch.uint8, device=DEV)
+    slots = np.arange(page - n, page, dtype=np.int32)
+    Q.qlin_kv_write(d, pool, dev(k), dev(v), dev(slots))
+    small = D.Cache(3, 16, 1, dim, kb, vb)
+    small.write(k, v, range(n))
+    for got, ref in zip(Q.qlin_kv_read(d, pool, dev(slots)), small.read(range(n))):
+        assert np.array_equal(got.cpu().numpy(), ref)
+    scale = float(np.float32(dim ** -0.5))
+    assert (small.values(0, range(n))[:, 0].astype(np.float64) @ q[0].T.astype(np.float64) * scale).min() > 50
+    got = Q.qlin_attn_decode(d, pool, dev(q), dev(np.zeros((1, 1), np.int32)), dev(np.array([page], np.int32)))
+    ref, tol = D.attention64(small, q, np.arange(3)[None], [n], scale)
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert (err <= tol).all(), f"worst error / bound {float((err / tol).max()):.3f}"
