@@ -518,8 +518,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
   uint8_t* const ring_ptr = smem + warp * S * C::kStage;
   const uint32_t ring = smem_addr(ring_ptr);
 
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ int lens[kLensCached];
   __shared__ uint32_t signs[4 * NG];
   if (a.sign_bits && threadIdx.x < 4 * NG) signs[threadIdx.x] = a.sign_bits[threadIdx.x];
@@ -1014,8 +1014,8 @@ __global__ void __launch_bounds__(W * 32) attn_join_kernel(const __grid_constant
   __shared__ __align__(16) float sums[NG][W][kGroup];
   __shared__ float2 sml[NG][W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = blockIdx.y;
-  grid_launch_dependents();
   grid_dependency_wait();  // every block: this grid's end stands for the first one's too
+  grid_launch_dependents();
   const int4 rec = __ldcg(a.records + blockIdx.x);
   if (q >= rec.y) return;
   float top[NG], den[NG], r[NG][4];

@@ -37,8 +37,10 @@ qlin_status record_cuda(cudaError_t e);
 bool overlap_enabled();
 
 // Launches a kernel as a programmatic dependent of the one before it on the stream: it may be set up
-// while that one ends, and its first statement must be grid_dependency_wait() (qlin_sm100.cuh), after
-// which everything is as in an ordinary launch.
+// while that one ends.  Before it touches memory every thread calls grid_dependency_wait()
+// (qlin_sm100.cuh), after which everything is as in an ordinary launch, and only after that wait
+// grid_launch_dependents(): a GEMV that overlaps reads its weights before its own wait, so it must not
+// start while kernels before this one still run.
 template <typename... Params, typename... Args>
 qlin_status launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                              const Args&... args) {

@@ -129,8 +129,8 @@ __device__ __forceinline__ int checked_slot(const KvArgs& a, int s, int t) {
 template <int L>
 __global__ void __launch_bounds__(kThreads, ctas(L)) kv_write_kernel(const __grid_constant__ KvArgs a) {
   constexpr int C = 16 / L;  // pieces of eight values a lane
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ uint4 masks[2 * L * C];
   if (a.sign_bits) fill_masks<L>(masks, a.sign_bits, a.c.dim / kGroup);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -244,8 +244,8 @@ __device__ __forceinline__ f32x2 dequant2(uint32_t a, uint32_t b, f32x2 inv_unit
 template <int L>
 __global__ void __launch_bounds__(kThreads, ctas(L)) kv_read_kernel(const __grid_constant__ KvArgs a) {
   constexpr int C = 16 / L;  // pieces of eight values a lane
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ uint4 masks[2 * L * C];
   if (a.sign_bits) fill_masks<L>(masks, a.sign_bits, a.c.dim / kGroup);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

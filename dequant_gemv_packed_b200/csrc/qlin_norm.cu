@@ -41,8 +41,8 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 // One row a block (blockDim.y = 1) or a warp (blockDim.x = 32); NP pieces a thread.
 template <int NP, bool kResidual>
 __global__ void __launch_bounds__(kMaxWarps * 32) rmsnorm_kernel(const NormArgs a) {
-  grid_launch_dependents();  // a dependent (a GEMV that overlaps) may fetch its weights meanwhile
   grid_dependency_wait();
+  grid_launch_dependents();  // a dependent (a GEMV that overlaps) may fetch its weights meanwhile
   __shared__ float part[kMaxWarps];
   const unsigned row = blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= (unsigned)a.rows) return;  // whole warps: blocks of several rows have one warp each

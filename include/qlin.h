@@ -115,9 +115,11 @@ int qlin_last_cuda_error(void);
  * packed weight, scales, zeros and sign bits, before that kernel has finished;
  * it waits for it before reading x or writing y.  This hides the launch and
  * ramp of back-to-back calls, as in a decode loop over layers.  Enable it only
- * if no kernel that writes the weight, scale, zero or sign buffers immediately
- * precedes a call on the same stream.  Process-wide; default off.  Returns the
- * previous setting. */
+ * if no kernel that writes the weight, scale, zero or sign buffers precedes a
+ * call on the same stream immediately, or with nothing but qlin_gemv calls
+ * between them (an ordinary launch or a copy between them, or any other call of
+ * this library, is enough).  Process-wide; default off.  Returns the previous
+ * setting. */
 int qlin_set_overlap(int enable);
 
 /* Bytes of the packed buffer for `desc` (codes, plus the block table for mixed
