@@ -410,7 +410,7 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* sig
                                            float (&r)[4], float den) {
   const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] *= inv;
+  for (int i = 0; i < 4; ++i) r[i] = fmaf(r[i], 0.f, r[i]) * inv;  // infinite: a value is, at 16 bits; NaN
   if (a.sign_bits) rotate4(r, signs, g, lane, true);
   const __half2 h0 = __floats2half2_rn(r[0], r[1]), h1 = __floats2half2_rn(r[2], r[3]);
   uint2 w;
@@ -813,6 +813,11 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           }
         }
       }
+      // An infinite score is an infinity among the query's or the key's values: NaN, and not a weight of zero.
+      // (Of 4- and 8-bit codes it comes as NaN, by the group's zero or the query's scale.)
+      if (KB == 16)
+#pragma unroll
+        for (int s = 0; s < NT; ++s) w[s][0] = fmaf(w[s][0], 0.f, w[s][0]), w[s][1] = fmaf(w[s][1], 0.f, w[s][1]);
       if (valid < kTile) {  // masked tokens: no weight, and nothing kept of their parameters
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -443,9 +443,10 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  * as 24-bit integers with one power-of-two scale per group of 128 (exact for values
  * within a factor 2^11 of the group's largest, others rounded at 2^-22 of it, as an
  * fp32 sum would round them).  The softmax weights (times the values' scales) enter
- * the value sums with 22 bits.  An infinity or NaN among a head's query, keys or
- * values within the length gives NaN there; what lies past the length has no
- * effect.  Deterministic.
+ * the value sums with 22 bits.  An infinity or NaN in a head's query or in one of
+ * its keys within the length makes all of the head's outputs NaN, one in a value
+ * those of its dimension (at 16 bits without sign bits) or of its group of 128;
+ * what lies past the length has no effect.  Deterministic.
  *   q     : device fp16, sequence b's heads [q_heads][head_dim] at element offset
  *           b * q_stride; q_stride >= q_heads * head_dim, a multiple of 8;
  *           q_heads a multiple of kv_heads;

@@ -95,3 +95,47 @@ def test_attention_far_inside_one_page(page, dim, kb, vb):
     ref, tol = D.attention64(small, q, np.arange(3)[None], [n], scale)
     err = np.abs(got.double().cpu().numpy() - ref)
     assert (err <= tol).all(), f"worst error / bound {float((err / tol).max()):.3f}"
+
+
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("group", [4, 8])
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 8), (4, 4)])
+def test_infinities_and_nan(kb, vb, group, rotate):
+    """One infinity or NaN in a query, a key or a value, in a sequence that is read whole and in one that is cut and
+    joined: NaN in the outputs that it has a part in, and the same bits in all others; past the length it has
+    no effect."""
+    rng = np.random.default_rng(kb + group)
+    heads, dim, page = 2, 256, 16
+    lens = [40, 700]
+    slots = [np.arange(48), np.arange(48, 48 + 704)]
+    table = np.zeros((2, 44), np.int32)
+    table[0, :3], table[1] = np.arange(3), np.arange(3, 47)
+    sb = dev(rng.integers(0, 2 ** 32, dim // 32, dtype=np.uint64).astype(np.uint32).view(np.int32)) if rotate else None
+    d = Q.KVDesc(47, page, heads, dim, kb, vb)
+    at = dev(np.concatenate(slots).astype(np.int32))
+    k, v = (rng.standard_normal((752, heads, dim)).astype(np.float16) for _ in range(2))
+    q = rng.standard_normal((2, heads * group, dim)).astype(np.float16)
+
+    def run(q, k, v):
+        pool = torch.zeros(Q.qlin_kv_cache_bytes(d), dtype=torch.uint8, device=DEV)
+        Q.qlin_kv_write(d, pool, dev(k), dev(v), at, sign_bits=sb)
+        return Q.qlin_attn_decode(d, pool, dev(q), dev(table), dev(np.array(lens, np.int32)), sign_bits=sb).cpu().numpy()
+
+    clean = run(q, k, v)
+    assert np.isfinite(clean).all()
+    for bad in (np.inf, -np.inf, np.nan):
+        for b in (0, 1):
+            for what in ("q", "k", "v", "past"):
+                x = {"q": q.copy(), "k": k.copy(), "v": v.copy()}
+                where = np.zeros(clean.shape, bool)
+                if what == "q":
+                    x["q"][b, group + 1, 130] = bad
+                    where[b, group + 1] = True
+                elif what == "past":
+                    x["k"][slots[b][lens[b]], 1, 130] = x["v"][slots[b][lens[b]], 1, 130] = bad
+                else:
+                    x[what][slots[b][lens[b] // 2], 1, 130] = bad
+                    where[b, group:, slice(0, 256) if what == "k" else 130 if kb == 16 and not rotate else slice(128, 256)] = True
+                got = run(x["q"], x["k"], x["v"])
+                assert np.array_equal(np.isnan(got), where), (what, bad, b)
+                assert np.array_equal(got[~where], clean[~where]), (what, bad, b)
