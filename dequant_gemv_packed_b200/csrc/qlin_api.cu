@@ -362,8 +362,10 @@ qlin_status qlin_attn_decode(const qlin_kv_desc* d, const void* cache, const uin
                              size_t workspace_bytes, qlin_stream_t st) {
   qlin_status r = check_attn(d, q_heads, B, max_pages);
   if (r != QLIN_OK) return r;
-  if (!cache || !q || !block_table || !seq_lens || !out || q == out || !std::isfinite(scale))
-    return QLIN_ERR_INVALID_ARG;
+  if (!cache || !q || !block_table || !seq_lens || !out || q == out) return QLIN_ERR_INVALID_ARG;
+  // Scores of finite values then stay below 256 * 65504 * (255 * 65504) * 2^40 = 2^89, within the kernel's
+  // range (running maxima start at -1e30) and far from fp32's.
+  if (!(std::fabs(scale) <= 0x1p40f)) return QLIN_ERR_INVALID_ARG;
   if (!row_stride_ok(q_stride, (int64_t)q_heads * d->head_dim)) return QLIN_ERR_SHAPE;
   if (!aligned16(cache) || !aligned16(q) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned16(out) ||
       !aligned16(sign_bits))

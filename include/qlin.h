@@ -456,6 +456,7 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  *           sets bit 25 of qlin_device_error;
  *   seq_lens : device int32 [B] (4-byte aligned).  A length <= 0 gives zeros; one
  *           beyond max_pages * page_size is cut there and sets bit 26;
+ *   scale : at most 2^40 in magnitude, so that every score is well inside fp32;
  *   out   : device fp16 [B][q_heads][head_dim], not q;
  *   workspace : >= qlin_attn_workspace_bytes(...) bytes, overwritten; calls that
  *           overlap on the GPU need one each.

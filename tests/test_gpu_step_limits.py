@@ -139,3 +139,23 @@ def test_infinities_and_nan(kb, vb, group, rotate):
                 got = run(x["q"], x["k"], x["v"])
                 assert np.array_equal(np.isnan(got), where), (what, bad, b)
                 assert np.array_equal(got[~where], clean[~where]), (what, bad, b)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 40, -2.0 ** 40])
+@pytest.mark.parametrize("kb,vb", [(16, 16), (8, 8), (4, 4)])
+def test_largest_scale(kb, vb, scale):
+    """The token of the largest score has all the weight, whatever the scores' size and sign.  The bound: the output's
+    rounding, and 2^-18 of s (q + |z|), at most twice the largest value, for the few fp32 steps of the quotient."""
+    rng = np.random.default_rng(kb)
+    c = D.Cache(2, 16, 1, 256, kb, vb)
+    c.write(rng.standard_normal((20, 1, 256)).astype(np.float16), rng.standard_normal((20, 1, 256)).astype(np.float16),
+            range(20))
+    q = (1000 * rng.standard_normal((1, 4, 256))).astype(np.float16)
+    d = Q.KVDesc(2, 16, 1, 256, kb, vb)
+    got = Q.qlin_attn_decode(d, dev(c.bytes.reshape(-1)), dev(q), dev(np.array([[0, 1]], np.int32)),
+                             dev(np.array([20], np.int32)), scale=scale).cpu().numpy()
+    s = np.sign(scale) * (c.values(0, range(20))[:, 0].astype(np.float64) @ q[0].T.astype(np.float64))
+    v = c.values(1, range(20))[:, 0].astype(np.float64)
+    for h in range(4):
+        ref = v[s[:, h].argmax()]
+        assert (np.abs(got[0, h] - ref) <= np.abs(ref) * (2.0 ** -11 + 2.0 ** -17) + np.abs(v).max() * 2.0 ** -17).all()
