@@ -23,3 +23,27 @@ ODD = ctypes.c_void_p(0x10008)  # 8-byte aligned
 def test_attention_refuses_scales_past_its_range(lib, scale):
     d = Q.KVDesc(4, 16, 2, 128, 8, 8)
     assert lib.qlin_attn_decode(d.ref(), P, P, 512, 4, P, 2, P, 1, None, scale, P2, P3, 1 << 40, None) == -1
+
+
+def attend(lib, d, pages, ws, size, group=2):
+    return lib.qlin_attn_decode(d.ref(), P, P, 512 * group, 2 * group, P, pages, P, 1, None, 1.0, P2, ws, size, None)
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+def test_attention_workspace(lib, dim):
+    """None for tables of up to 512 tokens, whose sequences are never cut; beyond, two pieces of each query of a block
+    (dim sums, maximum and denominator) for at least 148 CTAs, refused if missing, short or misaligned."""
+    d = Q.KVDesc(4, 16, 2, dim, 8, 8)
+    assert Q.qlin_attn_workspace_bytes(d, 4, 1, 32) == 0
+    sizes = {}
+    for group, block in ((1, 1), (2, 2), (4, 4), (8, 8), (9, 5), (16, 8)):
+        size = sizes[group] = Q.qlin_attn_workspace_bytes(d, 2 * group, 1, 33)
+        assert size >= 148 * 2 * block * (dim + 2) * 4
+        assert Q.qlin_attn_workspace_bytes(d, 2 * group, 7, 4096) == size
+        for pages in (33, 4096):
+            assert attend(lib, d, pages, None, size, group) == -6
+            assert attend(lib, d, pages, None, 0, group) == -6
+            assert attend(lib, d, pages, P3, size - 1, group) == -6
+            assert attend(lib, d, pages, ODD, size, group) == -4
+    assert sizes[1] < sizes[2] < sizes[4] < sizes[8] == sizes[16]
+    assert sizes[4] < sizes[9] < sizes[8]
