@@ -415,7 +415,8 @@ size_t qlin_kv_cache_bytes(const qlin_kv_desc* desc);
  *           differ: two tokens at one slot leave bytes of either there;
  *   sign_bits : device uint32 [head_dim/32], or NULL for no rotation; the cache
  *           must be read with the same.
- * T >= 1.  Slots that are not named keep their bytes. */
+ * T >= 1, and T * kv_heads * head_dim / 128 < 2^31 - 2^20 groups a side
+ * (QLIN_ERR_SHAPE beyond).  Slots that are not named keep their bytes. */
 qlin_status qlin_kv_write(const qlin_kv_desc* desc, void* cache, const uint16_t* k, const uint16_t* v,
                           int64_t k_stride, int64_t v_stride, const int32_t* slots, int32_t T,
                           const uint32_t* sign_bits, qlin_stream_t stream);
@@ -425,7 +426,8 @@ qlin_status qlin_kv_write(const qlin_kv_desc* desc, void* cache, const uint16_t*
  * scaling, then the signs).
  *   k, v  : device fp16 [T][kv_heads][head_dim], written entirely; a negative
  *           slot gives zeros, so does one past the pool, which sets bit 24 of
- *           qlin_device_error.  A slot may occur any number of times. */
+ *           qlin_device_error.  A slot may occur any number of times.
+ * T as in qlin_kv_write. */
 qlin_status qlin_kv_read(const qlin_kv_desc* desc, const void* cache, const int32_t* slots, int32_t T,
                          const uint32_t* sign_bits, uint16_t* k, uint16_t* v, qlin_stream_t stream);
 

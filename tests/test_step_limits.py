@@ -47,3 +47,13 @@ def test_attention_workspace(lib, dim):
             assert attend(lib, d, pages, ODD, size, group) == -4
     assert sizes[1] < sizes[2] < sizes[4] < sizes[8] == sizes[16]
     assert sizes[4] < sizes[9] < sizes[8]
+
+
+def test_cache_calls_refuse_more_groups_than_they_count(lib):
+    """2^31 - 2^20 groups a side and more; one less passes the check and would be launched."""
+    for heads, dim in ((2, 128), (1, 256), (8, 256), (1 << 20, 128)):
+        d = Q.KVDesc(1, 16, heads, dim, 4, 4)
+        groups = heads * dim // 128
+        for t in (-(-(2 ** 31 - 2 ** 20) // groups), 2 ** 31 // groups - 1, 2 ** 31 - 1):
+            assert lib.qlin_kv_write(d.ref(), P, P, P, heads * dim, heads * dim, P, t, None, None) == -3
+            assert lib.qlin_kv_read(d.ref(), P, P, t, None, P2, P3, None) == -3
