@@ -300,6 +300,8 @@ static qlin_status check_kv(const qlin_kv_desc* d) {
     return QLIN_ERR_SHAPE;
   if (d->head_dim != kGroup && d->head_dim != 2 * kGroup) return QLIN_ERR_SHAPE;
   if ((int64_t)d->num_pages * d->page_size > 0x7fffffffLL) return QLIN_ERR_SHAPE;  // a slot is an int32
+  // values of a token; at 4 bytes each (key and value) the pool's size then fits in 64 bits
+  if ((int64_t)d->kv_heads * d->head_dim > 0x7fffffffLL) return QLIN_ERR_SHAPE;
   const int k = d->k_bits, v = d->v_bits;
   const bool coded = (k == 4 || k == 8) && (v == 4 || v == 8);
   return coded || (k == 16 && v == 16) ? QLIN_OK : QLIN_ERR_UNSUPPORTED;

@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
     const int n = a.lens[b];
     if (n > a.cap && threadIdx.x == 0) atomicOr(&g_attn_error, kKvBadLength);
     if (n <= 0) {
-      for (int i = threadIdx.x; i < a.q_heads * D / 8; i += NW * 32)
+      for (int i = threadIdx.x; i < a.q_heads * (D / 8); i += NW * 32)  // q_heads < 2^31 / kItemExtra
         reinterpret_cast<uint4*>(a.out + (int64_t)b * a.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
       if (a.may_cut && a.by_item && threadIdx.x < a.items) a.records[b * a.items + threadIdx.x] = make_int4(0, 0, 0, 0);
     }

@@ -396,7 +396,7 @@ qlin_status qlin_linear_host(const qlin_desc* desc, const void* packed, const ui
 typedef struct {
   int32_t num_pages;  /* >= 1; num_pages * page_size < 2^31                    */
   int32_t page_size;  /* tokens a page holds: a positive multiple of 16        */
-  int32_t kv_heads;   /* >= 1                                                  */
+  int32_t kv_heads;   /* >= 1; kv_heads * head_dim < 2^31                      */
   int32_t head_dim;   /* 128 or 256                                            */
   int32_t k_bits;     /* 4 or 8; or 16 for both sides                          */
   int32_t v_bits;

@@ -57,3 +57,17 @@ def test_cache_calls_refuse_more_groups_than_they_count(lib):
         for t in (-(-(2 ** 31 - 2 ** 20) // groups), 2 ** 31 // groups - 1, 2 ** 31 - 1):
             assert lib.qlin_kv_write(d.ref(), P, P, P, heads * dim, heads * dim, P, t, None, None) == -3
             assert lib.qlin_kv_read(d.ref(), P, P, t, None, P2, P3, None) == -3
+
+
+def test_cache_refuses_more_heads_than_it_counts(lib):
+    """A token of 2^31 values and more; up to there the pool's bytes are those of the layout, counted without a limit."""
+    for dim in (128, 256):
+        for heads, ok in ((2 ** 31 // dim - 1, True), (2 ** 31 // dim, False), (1 << 28, False), (2 ** 31 - 1, False)):
+            for pages, page in ((1, 16), (2 ** 27 - 1, 16), (1, 2 ** 31 - 16)):
+                for kb, vb, row in ((4, 4, dim + dim // 16), (16, 16, 4 * dim)):
+                    d = Q.KVDesc(pages, page, heads, dim, kb, vb)
+                    assert Q.qlin_kv_cache_bytes(d) == (pages * page * heads * row if ok else 0)
+                    if not ok:
+                        width = heads * dim
+                        assert lib.qlin_kv_write(d.ref(), P, P, P, width, width, P, 1, None, None) == -3
+                        assert lib.qlin_kv_read(d.ref(), P, P, 1, None, P2, P3, None) == -3
