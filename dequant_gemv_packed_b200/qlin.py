@@ -393,6 +393,8 @@ def _on(t: torch.Tensor, stream):
         return torch.cuda.device(t.device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the call's buffers on {t.device}")
     return torch.cuda.stream(stream)
 
 

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from dequant_gemv_packed_b200 import build as B
 from dequant_gemv_packed_b200 import qlin as Q
@@ -71,3 +72,23 @@ def test_cache_refuses_more_heads_than_it_counts(lib):
                         width = heads * dim
                         assert lib.qlin_kv_write(d.ref(), P, P, P, width, width, P, 1, None, None) == -3
                         assert lib.qlin_kv_read(d.ref(), P, P, 1, None, P2, P3, None) == -3
+
+
+def test_stream_of_another_device_is_refused():
+    """It was made current with its device, after which the call ran on the buffers' device in its default stream."""
+    class OnDevice0(torch.Tensor):
+        is_cuda = property(lambda self: True)
+        device = property(lambda self: torch.device("cuda", 0))
+
+        def get_device(self):
+            return 0
+
+    class Stream1:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    t = torch.zeros(1, 2, 128).as_subclass(OnDevice0)
+    d = Q.KVDesc(4, 16, 2, 128, 8, 8)
+    for call in (lambda s: Q.qlin_kv_write(d, t, t, t, t, stream=s), lambda s: Q.qlin_kv_read(d, t, t, stream=s),
+                 lambda s: Q.qlin_attn_decode(d, t, t, t, t, stream=s), lambda s: Q.qlin_rmsnorm(t, t, 1e-6, stream=s)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call(Stream1())
