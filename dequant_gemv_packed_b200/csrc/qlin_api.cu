@@ -387,7 +387,8 @@ qlin_status qlin_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint
   if (M < 1 || K < 8 || K % 8 || K > 65536) return QLIN_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(y) || !aligned16(residual_out))
     return QLIN_ERR_ALIGNMENT;
-  if (y == x || (residual && (y == residual || y == residual_out || residual_out == x))) return QLIN_ERR_INVALID_ARG;
+  if (y == x || y == weight || (residual && (y == residual || y == residual_out || residual_out == x || residual_out == weight)))
+    return QLIN_ERR_INVALID_ARG;
   return launch_rmsnorm(reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(residual),
                         reinterpret_cast<const __half*>(weight), eps, reinterpret_cast<__half*>(y),
                         reinterpret_cast<__half*>(residual_out), M, K, reinterpret_cast<cudaStream_t>(st));

@@ -92,3 +92,8 @@ def test_stream_of_another_device_is_refused():
                  lambda s: Q.qlin_attn_decode(d, t, t, t, t, stream=s), lambda s: Q.qlin_rmsnorm(t, t, 1e-6, stream=s)):
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             call(Stream1())
+
+
+def test_norm_refuses_to_write_over_its_weight(lib):
+    assert lib.qlin_rmsnorm(P, None, P2, 1e-6, P2, None, 1, 128, None) == -1
+    assert lib.qlin_rmsnorm(P, P3, P2, 1e-6, ctypes.c_void_p(0x40000), P2, 1, 128, None) == -1
