@@ -127,7 +127,11 @@ struct Cfg {
   static constexpr int kOther = kSmemQ + kSmemX + kSmemMl + kAlign;  // and room to align it
   static constexpr int fit(int ctas) { return (226 * 1024 / ctas - 4096 - kOther) / (kWarps * kStage); }
   static constexpr int kCtas = kSets == 2 && NT == 1 && KB < 16 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;  // per SM
-  static constexpr int kStages = fit(kCtas) > 6 ? 6 : fit(kCtas);
+  // One stage to read and one to fill are enough once a row has 8-bit codes: 32 x 8,000 tokens at 8 bits take
+  // 88.6 us and not 93.6 with three, 8 x 8,192 at 8/4 bits 14.1 and not 14.4, the call of 7 above 28.4 and not
+  // 29.1.  At 4 bits four take 62.9 us and two 63.7, 16-bit rows 80.6 with three and 81.0 with two (48 x 2,500).
+  static constexpr int kMostStages = KB < 16 && KB + VB > 8 ? 2 : 6;
+  static constexpr int kStages = fit(kCtas) > kMostStages ? kMostStages : fit(kCtas);
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kSmem = kRing + kOther;
   static constexpr int kGrid = kSms * kCtas;
