@@ -11,10 +11,10 @@
 // are exact, others rounded at 2^-22 of it, the rounding of an fp32 sum); each digit's
 // sum of products and sum xi are exact in int32, and the digits' sums meet in fp32.
 // Two digits, 2^-14 of the largest, would lose the small channels of a query with a large
-// one and move every output by 0.8e-4; the third costs four products a tile and group, 5 %
-// of the time where products bind (32 x 8,000 tokens, 8 bits: 93.5 us, 88.4 with two; 4 bits:
-// 62.6, 56.8).  The codes are the operand as stored (8 bits) or masked in place (4 bits;
-// the odd codes are 16 q in accumulators of their own).
+// one and move every output by 0.8e-4; the third costs four products a tile and group: 32 x
+// 8,000 tokens take 62.9 us at 4 bits and 57.0 with two, and at 8 bits, where HBM binds, 88.7
+// and 88.3.  The codes are the operand as stored (8 bits) or masked in place (4 bits; the odd
+// codes are 16 q in accumulators of their own).
 // Values: a nibble or byte masked into the low bits of an fp16 word is the
 // subnormal fp16 number q 2^-24 (a nibble at bits 4-7: q 2^-20), and one packed
 // multiplication makes a pair q 2^-9, exact.  (The subnormals would be exact
@@ -37,8 +37,9 @@
 // columns and one of the eight lowest digits (16-bit keys: one set of eight queries), with
 // queries 2t and 2t + 1 in lane t, and the columns of the value sums are the eight queries:
 // P's two digits, fp16(P) and fp16(P - fp16(P)), take a product each, into the same sums.
-// (One digit, 11 bits, moved every output by 1.2e-4 for 3 % less time: 24 x 9000 tokens of
-// 8 kv heads at 4 bits 70.0 us, 72.4 with two.)
+// One digit, 11 bits, would move every output by 1.2e-4 for 3 % less time: 24 x 9000 tokens of
+// 8 kv heads at 4 bits take 73.5 us.  (Both digits reach 2^-32 of the largest weight and no
+// further; with up to four queries the second digit, scaled, reaches 2^-43.)
 // In both movmatrix turns the packed pair into the next product's operand, and a
 // query's statistics live in the lanes that scale its sums.  More than eight queries
 // take another pass over the cache.
@@ -51,7 +52,7 @@
 // writes its piece of a cut item to the workspace (at most two: its first and last)
 // and the team of an item's first piece a record of it, and a dependent kernel joins
 // the pieces in order, a block a query.  (The last team to arrive joining them by
-// itself was measured slower: one CTA then reads them all, 6 us of 24 at 1 x 32773
+// itself was measured slower: one CTA then reads them all, 3.7 us more at 1 x 32773
 // tokens.)  Otherwise items stay whole, nothing is joined, and a team has the two, four
 // or eight warps that an estimate says end first.  A team's warps take every T-th tile
 // of its piece, each with its own statistics, joined in shared memory.
@@ -80,24 +81,23 @@ constexpr float kNone = -1e30f;   // running maximum of a warp that has seen no 
 constexpr int kWholeTiles = 32;   // items up to here are not cut
 constexpr int kMinShare = 16;     // tiles a team when they are
 // An item's cost beside its tiles, in tiles, for a team of T warps, fitted to short sequences (200 of
-// up to 509 tokens, 4 bits: 24.2 us; 25.7 with half the slope, 25.3 with 2 + 4 T) and to long ones
-// (24 x 9,000 tokens of 8 heads: 30.9, 38.3 and 31.5 us).
+// up to 509 tokens, 4 bits: 25.9 us; 27.5 with half the slope, 27.0 with 2 + 4 T) and to long ones
+// (24 of up to 9,000 tokens, eight queries on each of 8 kv heads, 4 bits: 35.0, 41.6 and 35.3 us).
 __device__ __forceinline__ int item_extra(int lt) { return 4 + (4 << lt); }
 // A warp's sums in shared memory: 16 values every 20 floats, which spreads both the lanes that
 // write (16 dimensions of a query each) and those that read over the banks.
 constexpr int kDumpRow = 8 * 20 + 8;  // of a query
 constexpr int kMaxTeams = 3 * kSms;  // teams when items are cut: one a CTA
 // Up to here records are of items and not of teams, which spares the join its empty blocks: 28 items
-// cut among 148 teams take 31.0 us and not 31.3, 8 take 16.0 and not 17.3.  128 items take 23.3 by
-// team, 23.9 by item: a team begins at most one cut item, so there are blocks without work either way.
+// cut among 148 teams take 1 % less, 8 take 8 % less, 128 items 2 % more: a team begins at most one cut item, so there are blocks without work either way.
 constexpr int kItemRecords = 64;
 static_assert(kItemRecords <= kMaxTeams);
 constexpr int kRecordBytes = kMaxTeams * 16;  // of the workspace: the item that each team is the first to cut
 
-// log2 of the least team's warps.  Without a team of two, 400 sequences of up to 60 tokens take 24.3 us
-// and not 18.7; without the choice a team's size would be a constant of the 4-warp shapes (100 x 500,
-// 256 wide: 24.9 and not 26.6).  A team of one: 21.5 and not 20.1 at 400 x 60, 57.3 and not 60.1 at
-// 1,000 x 130, for a longer code.
+// log2 of the least team's warps.  Without a team of two, 400 sequences of up to 60 tokens take 25.5 us
+// and not 19.4, 1,000 of up to 130 at 4 bits 76.1 and not 59.5 (where a team's size then is a constant,
+// with 4 warps, 100 x 500 tokens of 256 dimensions take 27.1 and not 28.2).  A team of one: 20.2 at
+// 400 x 60, 54.4 at 1,000 x 130, for a longer code.
 constexpr int kMinTeam = 1;
 
 template <int KB, int VB, int NG, int NT>
@@ -112,14 +112,15 @@ struct Cfg {
   static constexpr int kAlign = KB == 16 ? 256 : 128;
   static constexpr int kStage = ((kTileBytes > kDump ? kTileBytes : kDump) + 16 + kAlign - 1) / kAlign * kAlign;
   // 32 sums a lane (one group) leave room for 16 warps an SM at 128 registers; 64 (two) for 12 at
-  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 26.7 us; when it was
+  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 28.4 us; when it was
   // chosen 31.0, at 168 with spills 44.1, by two passes of four queries 33.0).  16-bit rows fill the rings: 8 warps.
   static constexpr int kSets = NG;
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
   static constexpr int kPlanes = 1024 * NT * NG;                // halves of the queries, or their two upper digits
   static constexpr int kOperand = KB == 16 ? kPlanes : kPlanes + kPlanes / 2;  // and the lowest digits
-  // Whether the lowest digits stay in registers through the tiles: 32 x 8,000 tokens at 4 bits take 62.6 us
-  // and not 64.8; the other shapes would spill.
+  // Whether the lowest digits stay in registers through the tiles: 32 x 8,000 tokens at 4 bits take 62.9 us
+  // and not 64.8; the other shapes would spill.  (As it is, 12 to 14 words a thread spill with eight queries
+  // on one group of 8-bit keys, at 128 registers, and with four on two groups, at 168; none elsewhere.)
   static constexpr bool kLowHeld = KB < 16 && NT == 1 && NG == 1;
   static constexpr int kSmemQ = (kWarps >> kMinTeam) * kOperand;          // of each team
   static constexpr int kSmemX = (kWarps >> kMinTeam) * kRowQ * NG * 8;    // (scale, sum) of each query, a team
@@ -151,7 +152,7 @@ struct AttnArgs {
   float* ws;  // [teams][2] slots of [qper][dim + 4]: sums, then maximum and denominator per group
   float scale_log2e;
   int32_t q_heads, max_pages, batch, cap;  // cap: tokens the table can hold
-  int32_t group, items, nqb, qper;  // queries a kv head;             // (head, query block) pairs of a sequence; blocks; queries a block
+  int32_t group, items, nqb, qper;  // queries a kv head; (head, query block) pairs of a sequence; blocks; queries a block
   int32_t page_shift;                      // log2 of a page's tiles; -1: no power of two
   int32_t by_item;                         // records are of items
   int32_t may_cut;                         // the table has room for more than kWholeTiles tiles
@@ -202,7 +203,7 @@ __device__ __forceinline__ Plan make_plan(const AttnArgs& a, int* lens, int grid
   p.lt = 31 - __clz(warps);
   if (!p.cut) {
     // the longest item on one team, or as many as a team gets of the average one, in tiles of a
-    // warp: the least.  Whole numbers of items: 64 sequences of up to 300 tokens take 10.2 us, 12.8
+    // warp: the least.  Whole numbers of items: 64 sequences of up to 300 tokens take 10.7 us, 26 % more
     // by the sum of the costs over all warps.
     const float mean = live ? (float)(n * a.items) * rcp((float)live) : 0.f;
     float best = INFINITY;
@@ -424,8 +425,8 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, const uint32_t* sig
 }
 
 // Sums of query j, dimensions 4 lane .. 4 lane + 3 of a group, over a team's T of at most W warps.
-// Unrolled, so that the loads do not wait for one another: the call of 1 x 32,773 tokens takes 15.6 us
-// and not 16.5, that of 7 of 256 dimensions and eight queries 26.7 and not 30.4.
+// Unrolled, so that the loads do not wait for one another: the call of 1 x 32,773 tokens takes 0.9 us
+// less, that of 7 of 256 dimensions and eight queries 3.7.
 template <int W>
 __device__ __forceinline__ void gather(const uint8_t* smem, const int* dump_at, const float2* sml, int T, int j,
                                         int lane, float (&r)[4], float& top, float& den) {
@@ -1092,8 +1093,8 @@ qlin_status launch(const AttnArgs& a, cudaStream_t s) {
   }
   const qlin_status r = launch_dependent(attn_kernel<KB, VB, NG, NT>, C::kGrid, C::kWarps * 32, C::kSmem, s, a);
   if (r != QLIN_OK || !a.may_cut) return r;
-  // Few items have many pieces.  16 warps a block and not 8: 17.0 us and not 17.7 at 8 items of 18
-  // pieces; 4 and not 8: 14.3 us and not 15.0 at 64 items of 2 or 3.
+  // Few items have many pieces.  16 warps a block and not 8: 0.7 us less at 8 items of 18 pieces;
+  // 4 and not 8: 0.7 us less at 64 items of 2 or 3.
   const int64_t items = (int64_t)a.batch * a.items;
   if (items <= 8) return launch_dependent(attn_join_kernel<NG, 16>, dim3(items, a.qper), 16 * 32, 0, s, a);
   if (items <= 32) return launch_dependent(attn_join_kernel<NG, 8>, dim3(items, a.qper), 8 * 32, 0, s, a);

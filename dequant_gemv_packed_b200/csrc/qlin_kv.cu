@@ -28,7 +28,9 @@
 // left out.  With 574 instructions a warp of four groups it took 84; two-
 // value operations, constants in place of divisions and four lanes a group brought
 // it here.  Four lanes against eight: 16,384 unrotated wide tokens written and read
-// 41.1 us against 48.8, 16 tokens 6.3 against 5.6.
+// 41.2 us against 48.8; eight are 0.7 us better at 16 tokens (5.2).  A write alone:
+// 16 tokens 2.3 us; 16,384 tokens of 8 heads at 8 bits 22.3 not rotated, 33.2 rotated,
+// at 16 bits 23.7 (a read of those 24.5).
 #include "qlin_kv.cuh"
 #include "qlin_sm100.cuh"
 
