@@ -24,8 +24,8 @@
 //   out_d = (sum_t P_t q_v - z_v P_t) / sum_t P_t / s_v,
 // and m follows the maximum of score + log2 s_v: P is the weight that the sum is
 // really made of, whatever the sizes of the scales.  m is kept 7 to 15 binary orders
-// below the maximum and moved only when a score exceeds it by 15, which a vote
-// decides: after the first tile that is rare.
+// below the maximum (4 to 12 where lo 2^15 has to stay within fp16) and moved only when
+// a score exceeds it by 15 (12), which a vote decides: after the first tile that is rare.
 //
 // The eight columns of the products.  S^T = K Q^T has the tile's 16 tokens as rows,
 // O^T = V^T P^T 16 dimensions; lane (g, t) of an accumulator has columns 2t, 2t + 1.
@@ -36,10 +36,13 @@
 // Five to eight queries (NT = 2): the keys' products take two sets of (query, digit)
 // columns and one of the eight lowest digits (16-bit keys: one set of eight queries), with
 // queries 2t and 2t + 1 in lane t, and the columns of the value sums are the eight queries:
-// P's two digits, fp16(P) and fp16(P - fp16(P)), take a product each, into the same sums.
-// One digit, 11 bits, would move every output by 1.2e-4 for 3 % less time: 24 x 9000 tokens of
-// 8 kv heads at 4 bits take 73.5 us.  (Both digits reach 2^-32 of the largest weight and no
-// further; with up to four queries the second digit, scaled, reaches 2^-43.)
+// P's two digits, hi = fp16(P) and lo = P - hi, take a product each into the same sums.  hi meets
+// the codes as q 2^-9; lo, times 2^15, meets them as masked, q 2^-24 (nibbles at bits 4-7: lo 2^11
+// and q 2^-20; the last bits that subnormal operands cost lie far below hi's).  Scaled, lo stays
+// clear of fp16's own subnormals, and a small weight keeps its bits down to 2^-40 of the largest;
+// unscaled it ended at 2^-32, too little where the largest is a token with a scale 2^20 times the
+// others' and zeros in some dimensions.  One digit, 11 bits, would move every output by 1.2e-4.
+// 24 x 9000 tokens of 8 kv heads at 4 bits take 75.3 us, 73.4 with lo unscaled, 70.0 with one digit.
 // In both movmatrix turns the packed pair into the next product's operand, and a
 // query's statistics live in the lanes that scale its sums.  More than eight queries
 // take another pass over the cache.
@@ -107,20 +110,22 @@ struct Cfg {
   static constexpr int kPar = KB == 16 ? 0 : 8 * NG;
   static constexpr int kOffV = kTile * kRowK, kOffPar = kOffV + kTile * kRowV;
   static constexpr int kRowQ = 4 * NT;                  // queries
+  // log2 of the largest weight over m: below 2^12 half a step of fp16 is at most 1, and lo 2^15 no more than 2^15
+  static constexpr float kTop = NT == 2 && VB < 16 ? 12.f : 15.f;
   static constexpr int kTileBytes = kOffPar + kTile * kPar, kDump = 4 * kDumpRow * 4;
   // and a word: the tile's tokens; multiples of the longest row, so that swizzles apply to addresses
   static constexpr int kAlign = KB == 16 ? 256 : 128;
   static constexpr int kStage = ((kTileBytes > kDump ? kTileBytes : kDump) + 16 + kAlign - 1) / kAlign * kAlign;
   // 32 sums a lane (one group) leave room for 16 warps an SM at 128 registers; 64 (two) for 12 at
-  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 28.4 us; when it was
+  // 168, or 8 at 255 with eight queries (7 x 20,011 tokens at most, 8/4 bits: 29.1 us; when it was
   // chosen 31.0, at 168 with spills 44.1, by two passes of four queries 33.0).  16-bit rows fill the rings: 8 warps.
   static constexpr int kSets = NG;
   static constexpr int kWarps = (kSets > 1 || KB == 16) ? 4 : 8;
   static constexpr int kPlanes = 1024 * NT * NG;                // halves of the queries, or their two upper digits
   static constexpr int kOperand = KB == 16 ? kPlanes : kPlanes + kPlanes / 2;  // and the lowest digits
   // Whether the lowest digits stay in registers through the tiles: 32 x 8,000 tokens at 4 bits take 62.9 us
-  // and not 64.8; the other shapes would spill.  (As it is, 12 to 14 words a thread spill with eight queries
-  // on one group of 8-bit keys, at 128 registers, and with four on two groups, at 168; none elsewhere.)
+  // and not 64.8; the other shapes would spill.  (As it is, 12 to 25 words a thread spill with eight queries
+  // on one group of 8-bit keys or values, at 128 registers, and 12 with four on two groups, at 168.)
   static constexpr bool kLowHeld = KB < 16 && NT == 1 && NG == 1;
   static constexpr int kSmemQ = (kWarps >> kMinTeam) * kOperand;          // of each team
   static constexpr int kSmemX = (kWarps >> kMinTeam) * kRowQ * NG * 8;    // (scale, sum) of each query, a team
@@ -129,8 +134,8 @@ struct Cfg {
   static constexpr int fit(int ctas) { return (226 * 1024 / ctas - 4096 - kOther) / (kWarps * kStage); }
   static constexpr int kCtas = kSets == 2 && NT == 1 && KB < 16 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;  // per SM
   // One stage to read and one to fill are enough once a row has 8-bit codes: 32 x 8,000 tokens at 8 bits take
-  // 88.6 us and not 93.6 with three, 8 x 8,192 at 8/4 bits 14.1 and not 14.4, the call of 7 above 28.4 and not
-  // 29.1.  At 4 bits four take 62.9 us and two 63.7, 16-bit rows 80.6 with three and 81.0 with two (48 x 2,500).
+  // 88.6 us and not 93.6 with three, 8 x 8,192 at 8/4 bits 14.1 and not 14.4, the call of 7 above 0.7 us
+  // less.  At 4 bits four take 62.9 us and two 63.7, 16-bit rows 80.6 with three and 81.0 with two (48 x 2,500).
   static constexpr int kMostStages = KB < 16 && KB + VB > 8 ? 2 : 6;
   static constexpr int kStages = fit(kCtas) > kMostStages ? kMostStages : fit(kCtas);
   static constexpr int kRing = kWarps * kStages * kStage;
@@ -319,9 +324,10 @@ __device__ __forceinline__ uint32_t scaled(uint32_t pair, uint32_t mul) {
   return d;
 }
 constexpr uint32_t kLow = 0x78007800u, kHigh = 0x68006800u;  // 2^15, 2^11
-__device__ __forceinline__ uint32_t low4(uint32_t w) { return scaled(w & 0x000F000Fu, kLow); }
-__device__ __forceinline__ uint32_t high4(uint32_t w) { return scaled(w & 0x00F000F0u, kHigh); }
-__device__ __forceinline__ uint32_t low8(uint32_t w) { return scaled(w & 0x00FF00FFu, kLow); }
+constexpr uint32_t kLow4 = 0x000F000Fu, kHigh4 = 0x00F000F0u, kLow8 = 0x00FF00FFu;
+__device__ __forceinline__ uint32_t low4(uint32_t w) { return scaled(w & kLow4, kLow); }
+__device__ __forceinline__ uint32_t high4(uint32_t w) { return scaled(w & kHigh4, kHigh); }
+__device__ __forceinline__ uint32_t low8(uint32_t w) { return scaled(w & kLow8, kLow); }
 // Integer products: u8 codes, s8 digits.
 __device__ __forceinline__ void imma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -834,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           }
       }
 
-      uint32_t pb[NG][2], pl[NG][2];  // weights as operand; with NT = 2 their second digits
+      uint32_t pb[NG][2], pl[NG][2], ph[NG][2];  // weights as operand; with NT = 2 lo for codes at q 2^-24, at q 2^-20
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float y[NT][2], top[NT];
@@ -843,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
         for (int s = 0; s < NT; ++s) {
           y[s][0] = w[s][0] + lv[g][0], y[s][1] = w[s][1] + lv[g][1];
           top[s] = fmaxf(y[s][0], y[s][1]);
-          past |= top[s] > m[s][g] + 15.f;
+          past |= top[s] > m[s][g] + C::kTop;
         }
         if (__any_sync(0xffffffffu, past)) {
           float f[NT];
@@ -851,7 +857,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
           for (int s = 0; s < NT; ++s) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top[s] = fmaxf(top[s], __shfl_xor_sync(0xffffffffu, top[s], d));
-            const float next = fmaxf(m[s][g], top[s] - 7.f);
+            const float next = fmaxf(m[s][g], top[s] - (C::kTop - 8.f));
             f[s] = ex2(m[s][g] - next);
             m[s][g] = next;
             l[s][g] *= f[s], zc[s][g] *= f[s];
@@ -874,8 +880,14 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
 #pragma unroll
             for (int s = 0; s < NT; ++s) p[s] = ex2(y[s][i] - m[s][g]);
             pair = __floats2half2_rn(p[0], p[NT - 1]);
-            const __half2 rest = __floats2half2_rn(p[0] - __low2float(pair), p[NT - 1] - __high2float(pair));
+            const float r0 = p[0] - __low2float(pair), r1 = p[NT - 1] - __high2float(pair);
+            constexpr float low = VB == 16 ? 1.f : 0x1p15f, high = 0x1p11f;
+            const __half2 rest = __floats2half2_rn(r0 * low, r1 * low);
             pl[g][i] = movmatrix(*reinterpret_cast<const uint32_t*>(&rest));
+            if (VB == 4) {
+              const __half2 rest4 = __floats2half2_rn(r0 * high, r1 * high);
+              ph[g][i] = movmatrix(*reinterpret_cast<const uint32_t*>(&rest4));
+            }
 #pragma unroll
             for (int s = 0; s < NT; ++s) {
               l[s][g] = fmaf(p[s], rv[g][i], l[s][g]);
@@ -904,8 +916,8 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             mma(o[g][2 * half], x0, x2, y0, y2, pb[g][0], pb[g][1]);
             mma(o[g][2 * half + 1], x1, x3, y1, y3, pb[g][0], pb[g][1]);
             if (NT == 2) {
-              mma(o[g][2 * half], x0, x2, y0, y2, pl[g][0], pl[g][1]);
-              mma(o[g][2 * half + 1], x1, x3, y1, y3, pl[g][0], pl[g][1]);
+              mma(o[g][2 * half], x & kLow4, (x >> 8) & kLow4, y & kLow4, (y >> 8) & kLow4, pl[g][0], pl[g][1]);
+              mma(o[g][2 * half + 1], x & kHigh4, (x >> 8) & kHigh4, y & kHigh4, (y >> 8) & kHigh4, ph[g][0], ph[g][1]);
             }
           }
         } else if (VB == 8) {
@@ -920,7 +932,7 @@ __global__ void __launch_bounds__(Cfg<KB, VB, NG, NT>::kWarps * 32, Cfg<KB, VB, 
             const uint32_t x = __byte_perm(v0[j >> 1], v1[j >> 1], sel), y = __byte_perm(v2[j >> 1], v3[j >> 1], sel);
             const uint32_t x0 = low8(x), x1 = low8(x >> 8), y0 = low8(y), y1 = low8(y >> 8);
             mma(o[g][j], x0, x1, y0, y1, pb[g][0], pb[g][1]);
-            if (NT == 2) mma(o[g][j], x0, x1, y0, y1, pl[g][0], pl[g][1]);
+            if (NT == 2) mma(o[g][j], x & kLow8, (x >> 8) & kLow8, y & kLow8, (y >> 8) & kLow8, pl[g][0], pl[g][1]);
           }
         } else {
 #pragma unroll

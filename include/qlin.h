@@ -445,7 +445,7 @@ size_t qlin_attn_workspace_bytes(const qlin_kv_desc* desc, int32_t q_heads, int3
  * as 24-bit integers with one power-of-two scale per group of 128 (exact for values
  * within a factor 2^11 of the group's largest, others rounded at 2^-22 of it, as an
  * fp32 sum would round them).  The softmax weights (times the values' scales) enter
- * the value sums with 22 bits, or to 2^-32 of the largest.  An infinity or NaN in a head's query or in one of
+ * the value sums with 22 bits, or to 2^-40 of the largest (16 bits: 2^-32).  An infinity or NaN in a head's query or in one of
  * its keys within the length makes all of the head's outputs NaN, one in a value
  * those of its dimension (at 16 bits without sign bits) or of its group of 128;
  * what lies past the length has no effect.  Deterministic.

@@ -145,8 +145,11 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
     """(out, tolerance) [B, q_heads, dim] in float64, before the final rounding to fp16.
 
     The tolerance bounds what fp32 scores and 22-bit softmax weights may do:
-      * a weight enters the value sums as two fp16 digits: 2^-21 relative, or 2^-32 of
-        the largest for every token (digits that are subnormal);
+      * a weight, times the value's scale, enters the value sums as two fp16 digits:
+        2^-21 relative (within the last item's), or, where digits are subnormal, 2^-40
+        of the sequence's largest such product (16 bits, without scales: 2^-32 of the
+        largest weight).  For each token that moves the output by as much of q - z
+        (at 16 bits of the value);
       * a score is 128 or 256 products summed in fp32 (a rounding of 2^-24 of the
         magnitudes per step, sums of code products and of the zero's share apart);
       * for 4- and 8-bit keys x is rounded to 24-bit integers of unit 2^(E-21), E the
@@ -170,7 +173,7 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
             continue
         slots = table[b][t // cache.page].astype(np.int64) * cache.page + t % cache.page
         k, v = cache.values(0, slots).astype(np.float64), cache.values(1, slots).astype(np.float64)
-        mag = []
+        mag, par = [], None
         for side, x in ((0, k), (1, v)):  # s (q + |z|) at most: |value| + 2 s |z|
             m = np.abs(x)
             if coded:
@@ -191,7 +194,14 @@ def attention64(cache: Cache, q, table, lens, scale, sign_bits=None):
             p /= p.sum()
             o = p @ vh
             far = np.abs(vh - o)
-            d = (p * (2 * e + 2.0 ** -20)) @ far + 2.0 ** -32 * far.sum(0)
+            d = (p * (2 * e + 2.0 ** -20)) @ far
+            if coded:
+                for c in range(0, D, GROUP):
+                    sv = par[:, h // g, c // GROUP, 2]  # scales of the values
+                    steps = np.abs(vh[:, c:c + GROUP]) / np.where(sv > 0, sv, 1)[:, None]
+                    d[c:c + GROUP] += 2.0 ** -40 * (p * sv).max() * steps.sum(0)
+            else:
+                d = d + 2.0 ** -32 * p.max() * np.abs(vh).sum(0)
             d = d + (t.size + 64) * 2.0 ** -24 * (p @ mag[1][:, h // g]) + 2.0 ** -18 * np.abs(o)
             out[b, h] = R.T @ o
             tol[b, h] = np.abs(R.T) @ d

@@ -96,3 +96,19 @@ def test_weights_of_values_that_cancel(kb, vb, dim, group):
     q = rng.standard_normal((1, group, dim)).astype(np.float16)
     ref = check(c, q, np.zeros((1, 1), int), [3])
     assert np.abs(ref).max() < 200
+
+
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 8), (8, 4), (4, 8)])
+@pytest.mark.parametrize("dim,group", [(128, 4), (128, 5), (128, 8), (256, 8), (256, 12)])
+def test_small_values_beside_a_large_one_elsewhere(kb, vb, dim, group):
+    """One token whose values are 60,000 in half of a group's dimensions and zero in the others, among tokens with
+    values near 0.001: in those others the output is theirs alone, their scales 2^-23 of the large token's."""
+    rng = np.random.default_rng(kb + vb + dim + group)
+    c = D.Cache(2, 16, 1, dim, kb, vb)
+    v = 0.001 * rng.standard_normal((20, 1, dim))
+    v[7] = np.where(np.arange(dim) % 128 < 64, 60000.0, 0.0)  # its grid starts at zero: a zero is exact
+    k = 0.3 * rng.standard_normal((20, 1, dim))
+    c.write(k.astype(np.float16), v.astype(np.float16), range(20))
+    q = rng.standard_normal((1, group, dim)).astype(np.float16)
+    ref = check(c, q, np.arange(2)[None], [20])
+    assert np.abs(ref[..., np.arange(dim) % 128 >= 64]).max() < 0.002
