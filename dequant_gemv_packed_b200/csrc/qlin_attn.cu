@@ -84,8 +84,8 @@ constexpr float kNone = -1e30f;   // running maximum of a warp that has seen no 
 constexpr int kWholeTiles = 32;   // items up to here are not cut
 constexpr int kMinShare = 16;     // tiles a team when they are
 // An item's cost beside its tiles, in tiles, for a team of T warps, fitted to short sequences (200 of
-// up to 509 tokens, 4 bits: 25.9 us; 27.5 with half the slope, 27.0 with 2 + 4 T) and to long ones
-// (24 of up to 9,000 tokens, eight queries on each of 8 kv heads, 4 bits: 35.0, 41.6 and 35.3 us).
+// up to 509 tokens, 4 bits: 25.8 us; half the slope takes 6 % more, 2 + 4 T 4 % more) and to long ones
+// (24 of up to 9,000 tokens, eight queries on each of 8 kv heads, 4 bits: 35.3 us; 19 and 1 % more).
 __device__ __forceinline__ int item_extra(int lt) { return 4 + (4 << lt); }
 // A warp's sums in shared memory: 16 values every 20 floats, which spreads both the lanes that
 // write (16 dimensions of a query each) and those that read over the banks.
